@@ -22,6 +22,8 @@ LIB_PATH = os.path.join(_PKG, "libgwb.so")
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
+_F32 = ctypes.c_float
+_F64 = ctypes.c_double
 
 # name -> argument types (all return int gwb_status)
 SIGNATURES = {
@@ -42,6 +44,13 @@ SIGNATURES = {
     "gwb_gemv_w4a8": [_P, _I64, _P, _P, _I64, _I64, _P, _P],
     "gwb_qpack_sym_i8": [_P, _I64, _I64, _P, _P, _P],
     "gwb_gemm_i8i8": [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P],
+    "gwb_rmsnorm_quant_i8": [_P, _P, _P, _I64, _I64, _F64, _INT, _P, _P, _P, _P],
+    "gwb_kv_block_bytes": [_I64, _INT, _INT, _INT, _P],
+    "gwb_kv_write": [_P, _I64, _P, _I64, _P, _I64, _INT, _P, _I64, _I64, _I64, _INT, _INT, _INT, _P],
+    "gwb_kv_read": [_P, _I64, _I64, _I64, _INT, _INT, _INT, _P, _I64, _INT, _P, _P, _P],
+    "gwb_attn_decode_workspace": [_I64, _I64, _INT, _P],
+    "gwb_attn_decode": [_P, _I64, _I64, _I64, _INT, _P, _I64, _I64, _I64, _INT, _INT, _INT, _P, _I64, _I64, _P, _F32,
+                        _P, _P, _P, _I64, _P],
     "gwb_check_device_error": [_P],
     "gwb_debug_set_wait_cycles": [ctypes.c_ulonglong],
     "gwb_debug_inject_stream_k_stall": [_INT],
@@ -357,8 +366,179 @@ def gemm_i8i8(qx, sx, wq, sw, want_y=True, want_acc=False, y=None, acc=None):
     return y, acc
 
 
+# ------------------------------------------------------------------ norm, quantized paged cache, decode attention
+_HALF = {torch.bfloat16: 0, torch.float16: 1}   # gwb_dtype
+
+
+def _here(*tensors):
+    """All given tensors lie on the current CUDA device (the one whose stream the call goes to)."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _token_rows(t, name, shape, dtypes):
+    """Rows [T, heads, head_dim] whose heads are contiguous; returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape) if shape else '[tokens, heads, head_dim]'}")
+    T, H, D = t.shape
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {s})")
+    return s[0] if T > 1 else H * D
+
+
+def rmsnorm_quant_i8(x, weight, eps, residual=None, residual_out=None, qx=None, sx=None):
+    """RMS norm of x (+ residual) with a per-token int8 output: (qx int8 [M, K], sx fp32 [M], h or None).
+
+    x, residual bf16 or fp16 [M, K], weight [K] of the same dtype; h = x + residual, rounded once, is
+    written to residual_out (which may be x or residual).  qx and sx are what gemm_i8i8 / gemm_i8i4 take."""
+    _dev(x, "x", tuple(_HALF))
+    M, K = x.shape
+    dt = (x.dtype,)
+    _dev(weight, "weight", dt, (K,))
+    if residual is not None:
+        _dev(residual, "residual", dt, (M, K))
+        residual_out = _out(residual_out, "residual_out", (M, K), x.dtype, x.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual: the sum would be x itself")
+    qx = _out(qx, "qx", (M, K), torch.int8, x.device)
+    sx = _out(sx, "sx", (M,), torch.float32, x.device)
+    _here(x, weight, residual, residual_out, qx, sx)
+    _call("gwb_rmsnorm_quant_i8", _ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _HALF[x.dtype],
+          _ptr(residual_out), _ptr(qx), _ptr(sx), _stream())
+    return qx, sx, residual_out
+
+
+_block_bytes = {}
+
+
+def kv_block_bytes(page_size, head_dim, bits, group_size):
+    """Bytes of one page of one head of a quantized cache."""
+    key = (page_size, head_dim, bits, group_size)
+    n = _block_bytes.get(key)
+    if n is None:
+        out = _I64(0)
+        _call("gwb_kv_block_bytes", page_size, head_dim, bits, group_size, ctypes.byref(out))
+        n = _block_bytes[key] = out.value
+    return n
+
+
+def kv_cache(num_pages, heads, head_dim, page_size, bits, group_size, device="cuda"):
+    """An empty quantized paged cache: uint8 [num_pages, heads, block] (the block's layout: gwb.h).
+    Its memory is zeroed, so that rows never written read back as zeros."""
+    return torch.zeros(num_pages, heads, kv_block_bytes(page_size, head_dim, bits, group_size), dtype=torch.uint8,
+                       device=device)
+
+
+def _cache_check(cache, head_dim, bits, group_size):
+    """(pages, heads, page_size) of a cache."""
+    _dev(cache, "cache", (torch.uint8,))
+    if cache.dim() != 3:
+        raise ValueError(f"cache: shape {tuple(cache.shape)} != [pages, heads, block]")
+    pages, heads, block = cache.shape
+    granule = kv_block_bytes(16, head_dim, bits, group_size)
+    if block % granule != 0:
+        raise ValueError(f"cache: a block of {block} bytes does not hold granules of {granule} bytes "
+                         f"(head_dim {head_dim}, {bits} bits, group size {group_size})")
+    return pages, heads, block // granule * 16
+
+
+def kv_write(cache, slots, k, v, bits, group_size):
+    """Quantizes k, v [T, heads, head_dim] (bf16 or fp16, any token stride) into the cache at slots
+    (int64 [T], page * page_size + place; negative: the row is padding and left out)."""
+    ks = _token_rows(k, "k", None, _HALF)
+    T, H, D = k.shape
+    vs = _token_rows(v, "v", k.shape, (k.dtype,))
+    pages, heads, page_size = _cache_check(cache, D, bits, group_size)
+    if heads != H:
+        raise ValueError(f"k has {H} heads, the cache {heads}")
+    _dev(slots, "slots", (torch.int64,), (T,))
+    _here(cache, slots, k, v)
+    _call("gwb_kv_write", _ptr(k), ks, _ptr(v), vs, _ptr(slots), T, _HALF[k.dtype], _ptr(cache), pages, heads,
+          page_size, D, bits, group_size, _stream())
+    return cache
+
+
+def kv_read(cache, slots, head_dim, bits, group_size, dtype=torch.bfloat16, k=None, v=None):
+    """The cache's rows at slots (int64 [T]) as dense k, v [T, heads, head_dim]; zeros for negative slots."""
+    pages, heads, page_size = _cache_check(cache, head_dim, bits, group_size)
+    if dtype not in _HALF:
+        raise TypeError(f"dtype {dtype} not in {tuple(_HALF)}")
+    _dev(slots, "slots", (torch.int64,))
+    shape = (slots.numel(), heads, head_dim)
+    _dev(slots, "slots", (torch.int64,), shape[:1])
+    k = _out(k, "k", shape, dtype, cache.device)
+    v = _out(v, "v", shape, dtype, cache.device)
+    _here(cache, slots, k, v)
+    _call("gwb_kv_read", _ptr(cache), pages, heads, page_size, head_dim, bits, group_size, _ptr(slots), shape[0],
+          _HALF[dtype], _ptr(k), _ptr(v), _stream())
+    return k, v
+
+
+_ws_bytes = {}
+
+
+def attn_decode_workspace(q_heads, heads, head_dim):
+    """Bytes of attn_decode's workspace on the current device."""
+    key = (torch.cuda.current_device(), q_heads, heads, head_dim)
+    n = _ws_bytes.get(key)
+    if n is None:
+        out = _I64(0)
+        _call("gwb_attn_decode_workspace", q_heads, heads, head_dim, ctypes.byref(out))
+        n = _ws_bytes[key] = out.value
+    return n
+
+
+def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, out=None, lse=None, workspace=None):
+    """Attention of one new token a sequence over the quantized cache: [B, q_heads, head_dim] of q's dtype.
+
+    q [B, q_heads, head_dim] (bf16 or fp16, any sequence stride), page_table int32 [B, max_pages] (any row
+    stride), seq_lens int32 [B] (0: an empty row, zeros).  scale defaults to 1 / sqrt(head_dim).  lse, if
+    given, is an fp32 [B, q_heads] output.  workspace: a uint8 tensor of attn_decode_workspace() bytes that
+    no overlapping call uses; without one the call takes it from torch's allocator."""
+    qs = _token_rows(q, "q", None, _HALF)
+    B, HQ, D = q.shape
+    pages, heads, page_size = _cache_check(cache, D, bits, group_size)
+    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
+        raise ValueError("page_table must be a CUDA tensor (the library has no CPU path)")
+    if page_table.dtype != torch.int32:
+        raise TypeError(f"page_table: dtype {page_table.dtype} not in {(torch.int32,)}")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)} != [{B}, max_pages]")
+    max_pages = page_table.shape[1]
+    if max_pages > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table: a row's page ids must be contiguous")
+    ts = max(page_table.stride(0), max_pages) if B > 1 else max_pages
+    if B > 1 and page_table.stride(0) < max_pages:
+        raise ValueError("page_table: rows overlap")
+    _dev(seq_lens, "seq_lens", (torch.int32,), (B,))
+    out = _out(out, "out", (B, HQ, D), q.dtype, q.device)
+    if lse is not None:
+        _dev(lse, "lse", (torch.float32,), (B, HQ))
+    _here(q, cache, page_table, seq_lens, out, lse, workspace)
+    need = attn_decode_workspace(HQ, heads, D)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _dev(workspace, "workspace", (torch.uint8,))
+    _call("gwb_attn_decode", _ptr(q), qs, B, HQ, _HALF[q.dtype], _ptr(cache), pages, heads, page_size, D, bits,
+          group_size, _ptr(page_table), ts, max_pages, _ptr(seq_lens),
+          float(1.0 / D ** 0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(workspace),
+          workspace.numel(), _stream())
+    return out
+
+
 def check_device_error():
-    """Synchronizes the current stream; raises GwbError(TIMEOUT) if a bounded device wait gave up."""
+    """Synchronizes the current stream; raises GwbError(TIMEOUT) if a bounded device wait gave up, and
+    GwbError(INVALID_ARG) if a slot, page id or length in device memory was out of range."""
     _call("gwb_check_device_error", _stream())
 
 

@@ -40,6 +40,14 @@ gwb_status need(const void *p, const char *name) {
   return GWB_OK;
 }
 
+// Index arrays are read an element at a time: their own alignment is enough.
+gwb_status need_index(const void *p, const char *name, unsigned bytes) {
+  if (!p) return fail(GWB_ERR_INVALID_ARG, "%s must not be NULL", name);
+  if ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0)
+    return fail(GWB_ERR_ALIGN, "%s is not %u-byte aligned", name, bytes);
+  return GWB_OK;
+}
+
 gwb_status check_layout(int64_t N, int64_t K, int bits, int gs) {
   if (N < 0 || K < 0) return fail(GWB_ERR_INVALID_ARG, "negative size (N=%lld, K=%lld)", (long long)N, (long long)K);
   if (N >= kMaxDim || K >= kMaxDim) return fail(GWB_ERR_SHAPE, "N and K must be below 2^31");
@@ -84,7 +92,9 @@ const char *gwb_version(void) { return "group_wise_bit_b200 0.1 (sm_100a)"; }
 gwb_status gwb_check_device_error(void *stream) {
   unsigned int flag = 0;
   GWB_TRY(gwb::read_and_clear_device_error(as_stream(stream), &flag));
-  if (flag) return fail(GWB_ERR_TIMEOUT, "a bounded device-side wait gave up (flag 0x%x)", flag);
+  // (flag bits: ptx.cuh)
+  if (flag & 1u) return fail(GWB_ERR_TIMEOUT, "a bounded device-side wait gave up (flag 0x%x)", flag);
+  if (flag) return fail(GWB_ERR_INVALID_ARG, "a slot, page or length in device memory was out of range (flag 0x%x)", flag);
   return GWB_OK;
 }
 
@@ -448,6 +458,164 @@ gwb_status gwb_gemv_w4a8(const uint16_t *x, int64_t M, const uint32_t *wq, const
                     "gemv_w4a8: the staged activations of %lld tokens x K=%lld do not fit on chip; quantize with "
                     "quant_per_token_i8 and call gemm_i8i4", (long long)M, (long long)K)
              : s;
+}
+
+namespace {
+
+gwb_status check_dtype(int dtype) {
+  if (dtype != GWB_BF16 && dtype != GWB_F16) return fail(GWB_ERR_UNSUPPORTED, "dtype=%d is neither bf16 nor fp16", dtype);
+  return GWB_OK;
+}
+
+gwb_status check_cache(int64_t pages, int64_t heads, int64_t page_size, int head_dim, int bits, int gs) {
+  if (pages < 0 || heads < 0 || page_size < 0)
+    return fail(GWB_ERR_INVALID_ARG, "negative size (pages=%lld, heads=%lld, page_size=%lld)", (long long)pages,
+                (long long)heads, (long long)page_size);
+  if (bits != 4 && bits != 8) return fail(GWB_ERR_UNSUPPORTED, "cache bits=%d not in {4,8}", bits);
+  if (gs != 32 && gs != 64 && gs != 128) return fail(GWB_ERR_UNSUPPORTED, "group_size=%d not in {32,64,128}", gs);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(GWB_ERR_UNSUPPORTED, "head_dim=%d not in {64,128,256}", head_dim);
+  if (head_dim % gs != 0)
+    return fail(GWB_ERR_SHAPE, "head_dim=%d is not a multiple of group_size=%d", head_dim, gs);
+  if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0)
+    return fail(GWB_ERR_SHAPE, "page_size=%lld is not a power of two from 16 to 4096", (long long)page_size);
+  if (heads < 1 || heads > 65535) return fail(GWB_ERR_SHAPE, "heads=%lld not in 1..65535", (long long)heads);
+  if (pages >= kMaxDim) return fail(GWB_ERR_SHAPE, "pages must be below 2^31");
+  return GWB_OK;
+}
+
+// Rows [T][heads][head_dim] whose tokens are `stride` elements apart.
+gwb_status check_rows(const void *p, const char *name, int64_t stride, int64_t row) {
+  GWB_TRY(need(p, name));
+  if (stride < row) return fail(GWB_ERR_SHAPE, "%s: a token stride of %lld overlaps rows of %lld", name, (long long)stride,
+                                (long long)row);
+  if (stride % 8 != 0)
+    return fail(GWB_ERR_ALIGN, "%s: a token stride of %lld is not a multiple of 8 elements", name, (long long)stride);
+  return GWB_OK;
+}
+
+// The launch's blocks: 256 threads, 8 elements a thread, keys and values.
+gwb_status check_tokens(int64_t T, int64_t heads, int head_dim) {
+  if (T < 0) return fail(GWB_ERR_INVALID_ARG, "negative T=%lld", (long long)T);
+  if (T >= kMaxDim || T * heads * 2 * (head_dim / 8) / 256 >= kMaxDim - 1)
+    return fail(GWB_ERR_SHAPE, "T=%lld tokens of %lld heads exceed a launch", (long long)T, (long long)heads);
+  return GWB_OK;
+}
+
+}  // namespace
+
+gwb_status gwb_rmsnorm_quant_i8(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, int64_t M,
+                                int64_t K, double eps, int dtype, uint16_t *residual_out, int8_t *qx, float *sx,
+                                void *stream) {
+  if (M < 0 || K < 0) return fail(GWB_ERR_INVALID_ARG, "negative size (M=%lld, K=%lld)", (long long)M, (long long)K);
+  if (M >= kMaxDim || K >= kMaxDim) return fail(GWB_ERR_SHAPE, "M and K must be below 2^31");
+  GWB_TRY(check_dtype(dtype));
+  if (!(eps >= 0.0 && eps < 1e30)) return fail(GWB_ERR_INVALID_ARG, "eps=%g is not a finite number >= 0", eps);
+  if ((residual == nullptr) != (residual_out == nullptr))
+    return fail(GWB_ERR_INVALID_ARG, "residual and residual_out must both be given or both be NULL");
+  if (M == 0) return GWB_OK;
+  GWB_TRY(need(sx, "sx"));
+  if (K == 0) return zero_fill(sx, (size_t)M * 4, stream);
+  GWB_TRY(need(x, "x"));
+  GWB_TRY(need(weight, "weight"));
+  GWB_TRY(need(qx, "qx"));
+  if (residual) {
+    GWB_TRY(need(residual, "residual"));
+    GWB_TRY(need(residual_out, "residual_out"));
+  }
+  gwb::launch_rmsnorm_quant_i8(x, residual, weight, M, K, eps, dtype == GWB_F16, residual_out, qx, sx,
+                               as_stream(stream));
+  return gwb::check_launch("rmsnorm_quant_i8");
+}
+
+gwb_status gwb_kv_block_bytes(int64_t page_size, int head_dim, int bits, int group_size, int64_t *bytes) {
+  if (!bytes) return fail(GWB_ERR_INVALID_ARG, "bytes must not be NULL");
+  GWB_TRY(check_cache(0, 1, page_size, head_dim, bits, group_size));
+  *bytes = page_size / 16 * gwb::kv_granule_bytes(head_dim, bits, group_size);
+  return GWB_OK;
+}
+
+gwb_status gwb_kv_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                        const int64_t *slots, int64_t T, int dtype, void *cache, int64_t pages, int64_t heads,
+                        int64_t page_size, int head_dim, int bits, int group_size, void *stream) {
+  GWB_TRY(check_cache(pages, heads, page_size, head_dim, bits, group_size));
+  GWB_TRY(check_dtype(dtype));
+  GWB_TRY(check_tokens(T, heads, head_dim));
+  if (T == 0) return GWB_OK;
+  GWB_TRY(check_rows(k, "k", k_stride, heads * head_dim));
+  GWB_TRY(check_rows(v, "v", v_stride, heads * head_dim));
+  GWB_TRY(need_index(slots, "slots", 8));
+  if (pages > 0) GWB_TRY(need(cache, "cache"));
+  const gwb::KvCache c{cache, pages, heads, page_size, head_dim, bits, group_size};
+  gwb::launch_kv_write(k, k_stride, v, v_stride, slots, T, c, dtype == GWB_F16, as_stream(stream));
+  return gwb::check_launch("kv_write");
+}
+
+gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t page_size, int head_dim, int bits,
+                       int group_size, const int64_t *slots, int64_t T, int dtype, uint16_t *k, uint16_t *v,
+                       void *stream) {
+  GWB_TRY(check_cache(pages, heads, page_size, head_dim, bits, group_size));
+  GWB_TRY(check_dtype(dtype));
+  GWB_TRY(check_tokens(T, heads, head_dim));
+  if (T == 0) return GWB_OK;
+  GWB_TRY(need(k, "k"));
+  GWB_TRY(need(v, "v"));
+  GWB_TRY(need_index(slots, "slots", 8));
+  if (pages > 0) GWB_TRY(need(cache, "cache"));
+  const gwb::KvCache c{const_cast<void *>(cache), pages, heads, page_size, head_dim, bits, group_size};
+  gwb::launch_kv_read(c, slots, T, k, v, dtype == GWB_F16, as_stream(stream));
+  return gwb::check_launch("kv_read");
+}
+
+namespace {
+
+gwb_status check_heads(int64_t q_heads, int64_t heads) {
+  if (q_heads < 1 || q_heads > 65535) return fail(GWB_ERR_SHAPE, "q_heads=%lld not in 1..65535", (long long)q_heads);
+  if (q_heads % heads != 0)
+    return fail(GWB_ERR_SHAPE, "q_heads=%lld is not a multiple of the cache's heads=%lld", (long long)q_heads,
+                (long long)heads);
+  return GWB_OK;
+}
+
+}  // namespace
+
+gwb_status gwb_attn_decode_workspace(int64_t q_heads, int64_t heads, int head_dim, int64_t *bytes) {
+  if (!bytes) return fail(GWB_ERR_INVALID_ARG, "bytes must not be NULL");
+  GWB_TRY(check_cache(0, heads, 16, head_dim, 8, 32));
+  GWB_TRY(check_heads(q_heads, heads));
+  return gwb::attn_workspace_bytes(q_heads, heads, head_dim, bytes);
+}
+
+gwb_status gwb_attn_decode(const uint16_t *q, int64_t q_stride, int64_t B, int64_t q_heads, int dtype,
+                           const void *cache, int64_t pages, int64_t heads, int64_t page_size, int head_dim,
+                           int bits, int group_size, const int32_t *page_table, int64_t table_stride,
+                           int64_t max_pages, const int32_t *seq_lens, float scale, uint16_t *out, float *lse,
+                           void *workspace, int64_t workspace_bytes, void *stream) {
+  GWB_TRY(check_cache(pages, heads, page_size, head_dim, bits, group_size));
+  GWB_TRY(check_dtype(dtype));
+  GWB_TRY(check_heads(q_heads, heads));
+  if (B < 0 || max_pages < 0)
+    return fail(GWB_ERR_INVALID_ARG, "negative size (B=%lld, max_pages=%lld)", (long long)B, (long long)max_pages);
+  if (B >= ((int64_t)1 << 24) || max_pages >= kMaxDim)
+    return fail(GWB_ERR_SHAPE, "B must be below 2^24 and max_pages below 2^31");
+  if (table_stride < max_pages)
+    return fail(GWB_ERR_SHAPE, "table_stride=%lld is below max_pages=%lld", (long long)table_stride, (long long)max_pages);
+  if (!(scale > -1e30f && scale < 1e30f)) return fail(GWB_ERR_INVALID_ARG, "scale=%g is not finite", (double)scale);
+  if (B == 0) return GWB_OK;
+  GWB_TRY(check_rows(q, "q", q_stride, q_heads * head_dim));
+  GWB_TRY(need_index(seq_lens, "seq_lens", 4));
+  GWB_TRY(need(out, "out"));
+  GWB_TRY(need(workspace, "workspace"));
+  if (lse) GWB_TRY(need_index(lse, "lse", 4));
+  if (pages > 0) GWB_TRY(need(cache, "cache"));
+  if (max_pages > 0) GWB_TRY(need_index(page_table, "page_table", 4));
+  gwb::AttnCall c{};
+  c.q = q; c.q_stride = q_stride; c.B = B; c.q_heads = q_heads;
+  c.cache = gwb::KvCache{const_cast<void *>(cache), pages, heads, page_size, head_dim, bits, group_size};
+  c.table = page_table; c.table_stride = table_stride; c.max_pages = max_pages;
+  c.lens = seq_lens; c.scale = scale; c.f16 = dtype == GWB_F16;
+  c.out = out; c.lse = lse; c.ws = workspace; c.ws_bytes = workspace_bytes;
+  return gwb::launch_attn_decode(c, as_stream(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,62 @@
+// Host side of the decode attention: which instance a call takes, what the
+// device holds of it, and the workspace's size.
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "internal.h"
+
+namespace gwb {
+
+namespace {
+std::mutex g_mu;
+std::map<std::pair<int, const void *>, AttnSetup> g_setup;   // per device and kernel
+
+gwb_status sm_count(int *dev, int *sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  return e == cudaSuccess ? GWB_OK : fail(GWB_ERR_CUDA, "device lookup: %s", cudaGetErrorString(e));
+}
+}  // namespace
+
+gwb_status attn_setup(const void *kern, size_t smem, int threads, AttnSetup *out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_setup.find({dev, kern});
+  if (it == g_setup.end()) {
+    AttnSetup s{};
+    const gwb_status st = sm_count(&dev, &s.sms);
+    if (st != GWB_OK) return st;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&s.per_sm, kern, threads, smem);
+    if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode setup: %s", cudaGetErrorString(e));
+    if (s.per_sm < 1) return fail(GWB_ERR_CUDA, "attn_decode: %zu bytes of shared memory do not fit", smem);
+    it = g_setup.emplace(std::make_pair(dev, kern), s).first;
+  }
+  *out = it->second;
+  return GWB_OK;
+}
+
+// 16 heads a CTA where the group has more than 8 and the registers hold them
+// (head_dim <= 128): the codes are unpacked once for both 8-head tiles.
+int attn_tiles(int64_t group, int head_dim) { return group > 8 && head_dim <= 128 ? 2 : 1; }
+
+gwb_status attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, int64_t *bytes) {
+  int dev = 0, sms = 0;
+  const gwb_status s = sm_count(&dev, &sms);
+  if (s != GWB_OK) return s;
+  const int64_t heads = 8 * attn_tiles(q_heads / kv_heads, head_dim);
+  // two partials (sums, max and total a head) and a 16-byte record a CTA
+  *bytes = (int64_t)sms * kAttnMaxPerSm * (2 * 4 * heads * (head_dim + 2) + 16);
+  return GWB_OK;
+}
+
+gwb_status launch_attn_decode(AttnCall c, cudaStream_t st) {
+  c.tiles = attn_tiles(c.q_heads / c.cache.heads, c.cache.head_dim);
+  if (c.cache.bits == 4) return c.f16 ? launch_attn_4_fp16(c, st) : launch_attn_4_bf16(c, st);
+  return c.f16 ? launch_attn_8_fp16(c, st) : launch_attn_8_bf16(c, st);
+}
+
+}  // namespace gwb

@@ -1,0 +1,923 @@
+// Attention of one new token a sequence over the paged, quantized cache
+// (kv_layout.cuh), the length split over the whole GPU and joined.
+//
+// For query head h of kv head n, tokens t < len, groups g of the head dimension:
+//   key   k[t,d] = ck[t,d] * sk[t,g] + bk[t,g]     (codes, bf16 scale and bias; value v alike)
+//   S[t]  = sum_g sk[t,g] * (sum_{d in g} q[d] ck[t,d]) + bk[t,g] * (sum_{d in g} q[d])
+//   out   = sum_t p[t] v[t] / sum_t p[t],   p[t] = 2^(S[t] * scale * log2 e - m),  m a running max
+//   sum_t p v[t,d] = sum_t (p sv[t,g]) (cv[t,d] - Z) + sum_t p (bv[t,g] + Z sv[t,g]),  Z = 2^(bits-1)
+// so neither keys nor values are ever dequantized: the codes are the MMA's
+// operand and the group scales multiply 16-token score fragments and P.
+//
+// Work split.  The unit is a granule (16 tokens of one head, one contiguous
+// bulk copy).  The granules of all (sequence, head) pairs form one line, cut
+// into equal shares, one a CTA; every CTA finds its share from the lengths on
+// the device, so ragged batches and lengths that change between graph replays
+// are balanced and the host never reads a length.  A (sequence, head) that is
+// cut leaves one partial (fp32 sums, max, total) a piece, joined by a second,
+// dependent launch in a fixed order (no atomics: results are reproducible).
+// In a CTA the warps take granules in turn, each streaming its own through a
+// private ring of bulk copies, and join through shared memory.
+//
+// Codes enter the m16n8k16 fp16 MMA as subnormals: code bits in the low bits of
+// an fp16 are code * 2^-24, exactly, so unpacking is one AND per register (two
+// codes), with a shift for every other pair; the nibble at bits 4..7 stands for
+// 16 * code and its q is divided by 16 (exact) or its sum at the end.  Value
+// codes are centred with an exact HADD2, because the sum of uncentred codes is
+// far larger than the result and the tensor core truncates its accumulator.
+//
+// Precision.  q is scaled by a power of two per head into fp16 (exact for bf16
+// and fp16 but for elements 2^-27 below the largest).  Scores, maxima, totals
+// and outputs are fp32.  p is rounded to fp16 (2^-11) before it meets the codes,
+// and p * sv again; with PREC (fp16 outputs, whose own rounding is no coarser)
+// the remainders of both roundings go through a second MMA.  Value scales and
+// biases are normalized by a running power of two a group, so fp16's range
+// limits nothing but ratios inside one group's column.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "kv_layout.cuh"
+#include "ptx.cuh"
+
+namespace gwb {
+namespace {
+namespace attn {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLogP = 10.0f;      // P = p * 2^10 in fp16
+constexpr float kLogPMax = 14.0f;   // a larger P moves the running max
+
+struct Args {
+  const uint16_t *q;
+  int64_t q_stride;             // elements between sequences
+  const unsigned char *cache;
+  const int32_t *table;         // [B][table_stride] page ids
+  int64_t table_stride;
+  const int32_t *lens;          // [B]
+  uint16_t *out;                // [B][H * G][D]
+  float *lse;                   // [B][H * G] or NULL
+  float *ws;                    // partials, then records (see Ws)
+  int64_t pages;
+  int B, H, G, GH;              // GH: query heads of one chunk
+  int chunks;                   // chunks of a kv head's G query heads
+  int gshift, cap_gran;         // log2 of a page's granules; granules a table row can name
+  int depth;                    // ring slots a warp
+  int min_per;                  // least granules of a share
+  int f16;
+  float scale_log2;             // softmax scale * log2 e
+};
+
+// One record a CTA: the first piece of its share.
+struct Rec {
+  int b, hc, g0, n;             // sequence, head chunk, first granule, granules of the sequence (0: no piece)
+};
+// Workspace: [2 * CTAs] partials of GHP heads x (D sums, max, total), then [CTAs] Rec, then the share size.
+template <int D, int GHP>
+struct Ws {
+  static constexpr int kPart = GHP * (D + 2);   // floats of a partial
+};
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// D[16 x 8] += A[16 x 16] * B[16 x 8], fp16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                            *reinterpret_cast<const __half2 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// 2^n, n clamped into fp32's normal range.
+__device__ __forceinline__ float p2(int n) { return pow2f(max(-126, min(127, n))); }
+
+__device__ __forceinline__ float q_at(const uint16_t *p, int f16) {
+  return f16 ? __half2float(__ushort_as_half(*p)) : __uint_as_float((uint32_t)*p << 16);
+}
+
+// Where the share of a CTA begins: sequence, head chunk and granule, and the
+// share size.  Every thread sums a run of the lengths, one warp scan joins them.
+struct Start {
+  int b, hc, g, pad;
+  long long per, total, first;   // granules a share, of the whole line, before this CTA
+};
+
+__device__ __forceinline__ int granules(const Args &a, int b, bool report) {
+  const int len = max(0, __ldg(a.lens + b));
+  int n = len / kv::kTok + (len % kv::kTok != 0);
+  if (n > a.cap_gran) {
+    if (report) atomicOr(&g_device_error, kErrIndex);
+    n = a.cap_gran;
+  }
+  return n;
+}
+
+__device__ __forceinline__ void find_start(const Args &a, Start *st, long long *scan) {
+  const int tid = threadIdx.x, HC = a.H * a.chunks;
+  const int run = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  long long mine = 0;
+  for (int b = b0; b < b1; b++) mine += granules(a, b, blockIdx.x == 0);
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(kFull, inc, o);
+    if ((tid & 31) >= o) inc += t;
+  }
+  if ((tid & 31) == 31) scan[tid >> 5] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    if (w < (tid >> 5)) before += scan[w];
+    total += scan[w];
+  }
+  before *= HC;
+  total *= HC;
+  const long long per = max((long long)a.min_per, (total + gridDim.x - 1) / gridDim.x);
+  const long long first = per * blockIdx.x;
+  if (tid == 0) {
+    st->per = per;
+    st->total = total;
+    st->first = first;
+    st->b = a.B;
+  }
+  __syncthreads();
+  if (first < total && mine > 0 && first >= before && first < before + mine * HC) {
+    long long left = first - before;
+    for (int b = b0; b < b1; b++) {
+      const long long n = granules(a, b, false);
+      if (left < n * HC) {
+        st->b = b;
+        st->hc = (int)(left / n);
+        st->g = (int)(left - (long long)st->hc * n);
+        break;
+      }
+      left -= n * HC;
+    }
+  }
+  __syncthreads();
+}
+
+// The stream of granules one warp copies: within a piece every kWarps-th, then
+// the next piece of the CTA's share.
+struct Cursor {
+  int b, hc, g, end;            // current piece; granules [g, end) are left to this warp
+  long long left;               // granules of the share behind this piece
+  int n;                        // granules of sequence b
+  int page;                     // page id of granule g (loaded one granule ahead)
+};
+
+__device__ __forceinline__ void cursor_page(const Args &a, Cursor &c) {
+  if (c.g < c.end) c.page = __ldg(a.table + (int64_t)c.b * a.table_stride + (c.g >> a.gshift));
+}
+// Opens the piece that starts at granule g of (b, hc), skipping empty sequences.
+__device__ __forceinline__ void cursor_open(const Args &a, Cursor &c, int g, int warp) {
+  while (c.left > 0) {
+    if (c.b >= a.B) { c.left = 0; break; }
+    c.n = granules(a, c.b, false);
+    if (c.n > 0) {
+      const int len = (int)min((long long)(c.n - g), c.left);
+      c.left -= len;
+      c.end = g + len;
+      c.g = g + warp;
+      cursor_page(a, c);
+      return;
+    }
+    c.b++;
+    c.hc = 0;
+  }
+  c.g = c.end = 0;
+}
+__device__ __forceinline__ void cursor_next_piece(const Args &a, Cursor &c, int warp) {
+  if (c.left <= 0) { c.g = c.end = 0; return; }
+  if (++c.hc == a.H * a.chunks) {
+    c.hc = 0;
+    c.b++;
+  }
+  cursor_open(a, c, 0, warp);
+}
+// Leaves the cursor on a granule of this warp, or at the end (g == end, left == 0).
+__device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int warp) {
+  while (c.g >= c.end && c.left > 0) cursor_next_piece(a, c, warp);
+}
+
+template <int BITS, int D, int GS, int NT, bool PREC>
+struct Kernel {
+  static constexpr kv::Layout L = kv::layout(BITS, D, GS);
+  static constexpr int NG = L.NG;
+  static constexpr int GB = L.granule;
+  static constexpr int KM = D / 16;                       // score MMAs a granule and n-tile
+  static constexpr int VB = BITS == 4 ? D / 32 : D / 16;  // value blocks (8 lanes x 16 bits a token)
+  static constexpr int MPB = BITS == 4 ? 2 : 1;           // MMAs a value block
+  static constexpr int DB = D / VB;                       // dimensions of a value block
+  static constexpr int GHP = 8 * NT;
+  static constexpr int SROW = D + 4;                      // floats of a head's row in the join buffer
+  static constexpr int kJoin = kWarps * GHP * (SROW + 2) * 4;
+
+  // One warp's state of the current piece.
+  struct State {
+    float acc[VB * MPB][NT][4];
+    float bacc[NT][4];            // row r < NG: sum of P * (bias + Z scale) of group r
+    float m10[NT][2], l[NT][2];   // running max (log2, minus kLogP) and this lane's total, heads 8 nt + 2c, +1
+    int E[NG];                    // value scales and biases are held over 2^E
+  };
+
+  static __device__ __forceinline__ void reset(State &s) {
+#pragma unroll
+    for (int i = 0; i < VB * MPB; i++)
+#pragma unroll
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) s.acc[i][t][j] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) s.bacc[t][j] = 0.0f;
+      s.m10[t][0] = s.m10[t][1] = -INFINITY;
+      s.l[t][0] = s.l[t][1] = 0.0f;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; g++) s.E[g] = -100;
+  }
+
+  // One granule: scores, running max, P, values.  `valid`: its tokens in front of the length.
+  static __device__ __forceinline__ void granule(const unsigned char *sm, int valid, const uint32_t (&qf)[KM][NT][2],
+                                                 const float (&qsum)[NG][NT][2], const float (&sf)[NT][2], State &s) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    // ---- scores: 16 tokens x 8 heads, fp32, a group at a time
+    float sc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) sc[t][j] = 0.0f;
+    uint32_t km[2][NG];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(sm + 2 * L.code_bytes) + (r + 8 * h) * NG;
+      if constexpr (NG % 4 == 0) {
+#pragma unroll
+        for (int g = 0; g < NG; g += 4) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(p + g);
+          km[h][g] = u.x; km[h][g + 1] = u.y; km[h][g + 2] = u.z; km[h][g + 3] = u.w;
+        }
+      } else if constexpr (NG == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        km[h][0] = u.x; km[h][1] = u.y;
+      } else {
+        km[h][0] = p[0];
+      }
+    }
+    constexpr int WG = GS * BITS / 128;             // words (of a lane's row) a group
+    float ga[NT][4];
+#pragma unroll
+    for (int a = 0; a < L.NW / (4 * L.VW); a++) {
+      uint32_t w[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(sm) + ((a * 16 + r + 8 * h) * 4 + c) * L.VW;
+        if constexpr (L.VW == 4) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(p);
+          w[h][0] = u.x; w[h][1] = u.y; w[h][2] = u.z; w[h][3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(p);
+          w[h][0] = u.x; w[h][1] = u.y;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < L.VW; v++) {
+        const int i = a * L.VW + v;                 // word column 4 i + c of the row
+        if (i % WG == 0)
+#pragma unroll
+          for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) ga[t][j] = 0.0f;
+        if constexpr (BITS == 4) {
+          const uint32_t x0 = w[0][v], x1 = w[1][v], y0 = x0 >> 8, y1 = x1 >> 8;
+#pragma unroll
+          for (int t = 0; t < NT; t++) {
+            mma(ga[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[2 * i][t][0],
+                qf[2 * i][t][1]);
+            mma(ga[t], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qf[2 * i + 1][t][0],
+                qf[2 * i + 1][t][1]);
+          }
+        } else {
+          const uint32_t x0 = w[0][v], x1 = w[1][v];
+#pragma unroll
+          for (int t = 0; t < NT; t++)
+            mma(ga[t], x0 & 0x00ff00ffu, x1 & 0x00ff00ffu, (x0 >> 8) & 0x00ff00ffu, (x1 >> 8) & 0x00ff00ffu,
+                qf[i][t][0], qf[i][t][1]);
+        }
+        if (i % WG == WG - 1) {
+          const int g = i / WG;
+#pragma unroll
+          for (int t = 0; t < NT; t++) {
+            sc[t][0] = fmaf(ga[t][0], bf_lo(km[0][g]), fmaf(qsum[g][t][0], bf_hi(km[0][g]), sc[t][0]));
+            sc[t][1] = fmaf(ga[t][1], bf_lo(km[0][g]), fmaf(qsum[g][t][1], bf_hi(km[0][g]), sc[t][1]));
+            sc[t][2] = fmaf(ga[t][2], bf_lo(km[1][g]), fmaf(qsum[g][t][0], bf_hi(km[1][g]), sc[t][2]));
+            sc[t][3] = fmaf(ga[t][3], bf_lo(km[1][g]), fmaf(qsum[g][t][1], bf_hi(km[1][g]), sc[t][3]));
+          }
+        }
+      }
+    }
+    // ---- running max: moved only when a P would pass 2^14
+    const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8
+    const bool in0 = t0 < valid, in1 = t0 + 2 < valid;
+    float y[NT][4], top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        y[t][j] = (j < 2 ? in0 : in1) ? fmaf(sc[t][j], sf[t][j & 1], -s.m10[t][j & 1]) : -INFINITY;
+        top = fmaxf(top, y[t][j]);
+      }
+    if (__any_sync(kFull, top > kLogPMax)) {
+#pragma unroll
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float a0 = in0 ? sc[t][e] * sf[t][e] : -INFINITY, a1 = in1 ? sc[t][e + 2] * sf[t][e] : -INFINITY;
+          float mx = fmaxf(a0, a1);
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+          const float m = fmaxf(s.m10[t][e], mx - kLogP);
+          const float f = ex2(s.m10[t][e] - m);     // 0 the first time
+          s.m10[t][e] = m;
+          s.l[t][e] *= f;
+          s.bacc[t][e] *= f;
+#pragma unroll
+          for (int i = 0; i < VB * MPB; i++) {
+            s.acc[i][t][e] *= f;
+            s.acc[i][t][e + 2] *= f;
+          }
+          y[t][e] = in0 ? fmaf(sc[t][e], sf[t][e], -m) : -INFINITY;
+          y[t][e + 2] = in1 ? fmaf(sc[t][e + 2], sf[t][e], -m) : -INFINITY;
+        }
+    }
+    // ---- P, rounded to fp16 and transposed to the B operand: k = token, n = head
+    uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      float p[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        p[j] = ex2(y[t][j]);
+        s.l[t][j & 1] += p[j];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const uint32_t u = pack_h2(p[2 * h], p[2 * h + 1]);
+        if constexpr (PREC) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+          pl[t][h] = transpose8x8(pack_h2(p[2 * h] - f.x, p[2 * h + 1] - f.y));
+        }
+        ph[t][h] = transpose8x8(u);
+      }
+    }
+    // ---- value scales and biases of tokens 4c .. 4c+3; those behind the length are zero
+    const uint32_t k0 = (4 * c < valid ? 0xffffu : 0u) | (4 * c + 1 < valid ? 0xffff0000u : 0u);
+    const uint32_t k1 = (4 * c + 2 < valid ? 0xffffu : 0u) | (4 * c + 3 < valid ? 0xffff0000u : 0u);
+    const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG, *vb = vs + 32 * NG;
+    {
+      // the groups' powers of two: lane r checks group r % NG
+      const int g = r % NG;
+      uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32 + c * 8), b = *reinterpret_cast<const uint2 *>(vb + g * 32 + c * 8);
+      u.x &= k0; u.y &= k1; b.x &= k0; b.y &= k1;
+      const uint32_t su = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), bu = __vmaxu2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu);
+      // exponents that hold scale * 2^BITS and |bias| below 2^E
+      const int es = (int)max(su & 0xffffu, su >> 16) / 128 - 126 + BITS;
+      const int eb = (int)max(bu & 0xffffu, bu >> 16) / 128 - 126;
+      int need = max(es, eb);
+      need = min(need, 120);
+      int have = s.E[0];
+#pragma unroll
+      for (int i = 1; i < NG; i++) have = g == i ? s.E[i] : have;
+      if (__any_sync(kFull, need > have)) {
+#pragma unroll
+        for (int i = 0; i < NG; i++) {
+          int e = g == i ? need : -126;
+          e = __reduce_max_sync(kFull, e);
+          if (e > s.E[i]) {
+            e += 1;                                  // a little room, so that this stays rare
+            const float f = p2(s.E[i] - e);
+            s.E[i] = e;
+#pragma unroll
+            for (int j = 0; j < VB; j++)
+              if (j * DB / GS == i)
+#pragma unroll
+                for (int u2 = 0; u2 < MPB; u2++)
+#pragma unroll
+                  for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) s.acc[j * MPB + u2][t][k] *= f;
+            if (r == i)
+#pragma unroll
+              for (int t = 0; t < NT; t++) {
+                s.bacc[t][0] *= f;
+                s.bacc[t][1] *= f;
+              }
+          }
+        }
+      }
+      // sum of P * (bias + Z scale): one MMA, row g of A = group g's biases
+      int e = s.E[0];
+#pragma unroll
+      for (int i = 1; i < NG; i++) e = g == i ? s.E[i] : e;
+      const float f = p2(-e), z = (float)(1 << (BITS - 1));
+      uint32_t a0 = pack_h2(fmaf(bf_lo(u.x), z, bf_lo(b.x)) * f, fmaf(bf_hi(u.x), z, bf_hi(b.x)) * f);
+      uint32_t a2 = pack_h2(fmaf(bf_lo(u.y), z, bf_lo(b.y)) * f, fmaf(bf_hi(u.y), z, bf_hi(b.y)) * f);
+      if (r >= NG) a0 = a2 = 0u;
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        mma(s.bacc[t], a0, 0u, a2, 0u, ph[t][0], ph[t][1]);
+        if constexpr (PREC) mma(s.bacc[t], a0, 0u, a2, 0u, pl[t][0], pl[t][1]);
+      }
+    }
+    // ---- values: a group at a time, P * scale against the centred codes
+    constexpr uint32_t kC = BITS == 4 ? 0x80088008u : 0x80808080u;     // -Z * 2^-24 in both halves
+    constexpr uint32_t kC16 = 0x80808080u;                             // -16 Z * 2^-24 (4-bit)
+    const uint4 *vc = reinterpret_cast<const uint4 *>(sm + L.code_bytes) + lane;
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32 + c * 8);
+      u.x &= k0; u.y &= k1;
+      const float f = p2(BITS - s.E[g]);
+      const uint32_t s0 = pack_h2(bf_lo(u.x) * f, bf_hi(u.x) * f), s1 = pack_h2(bf_lo(u.y) * f, bf_hi(u.y) * f);
+      uint32_t b[NT][2], bl[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        b[t][0] = hmul2u(ph[t][0], s0);
+        b[t][1] = hmul2u(ph[t][1], s1);
+        if constexpr (PREC) {
+          bl[t][0] = hfma2u(pl[t][0], s0, hfma2u(ph[t][0], s0, b[t][0] ^ 0x80008000u));
+          bl[t][1] = hfma2u(pl[t][1], s1, hfma2u(ph[t][1], s1, b[t][1] ^ 0x80008000u));
+        }
+      }
+#pragma unroll
+      for (int j = g * GS / DB; j < (g + 1) * GS / DB; j++) {
+        // two blocks share a 16-byte load; the compiler keeps the second half
+        const uint4 q4 = vc[(j / 2) * 32];
+        const uint32_t x = j % 2 ? q4.z : q4.x, w = j % 2 ? q4.w : q4.y;
+        if constexpr (BITS == 4) {
+          const uint32_t x8 = x >> 8, w8 = w >> 8;
+          const uint32_t a0 = hadd2u(x & 0x000f000fu, kC), a1 = hadd2u(x & 0x00f000f0u, kC16);
+          const uint32_t a2 = hadd2u(w & 0x000f000fu, kC), a3 = hadd2u(w & 0x00f000f0u, kC16);
+          const uint32_t c0 = hadd2u(x8 & 0x000f000fu, kC), c1 = hadd2u(x8 & 0x00f000f0u, kC16);
+          const uint32_t c2 = hadd2u(w8 & 0x000f000fu, kC), c3 = hadd2u(w8 & 0x00f000f0u, kC16);
+#pragma unroll
+          for (int t = 0; t < NT; t++) {
+            mma(s.acc[2 * j][t], a0, a1, a2, a3, b[t][0], b[t][1]);
+            mma(s.acc[2 * j + 1][t], c0, c1, c2, c3, b[t][0], b[t][1]);
+            if constexpr (PREC) {
+              mma(s.acc[2 * j][t], a0, a1, a2, a3, bl[t][0], bl[t][1]);
+              mma(s.acc[2 * j + 1][t], c0, c1, c2, c3, bl[t][0], bl[t][1]);
+            }
+          }
+        } else {
+          const uint32_t a0 = hadd2u(x & 0x00ff00ffu, kC), a1 = hadd2u((x >> 8) & 0x00ff00ffu, kC);
+          const uint32_t a2 = hadd2u(w & 0x00ff00ffu, kC), a3 = hadd2u((w >> 8) & 0x00ff00ffu, kC);
+#pragma unroll
+          for (int t = 0; t < NT; t++) {
+            mma(s.acc[j][t], a0, a1, a2, a3, b[t][0], b[t][1]);
+            if constexpr (PREC) mma(s.acc[j][t], a0, a1, a2, a3, bl[t][0], bl[t][1]);
+          }
+        }
+      }
+    }
+  }
+
+  // Writes this warp's sums (value units, over 2^kLogP) and max / total to the join buffer.
+  static __device__ __forceinline__ void to_join(State &s, float *row_o, float *row_ml) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        float l = s.l[t][e];
+        l += __shfl_xor_sync(kFull, l, 4);
+        l += __shfl_xor_sync(kFull, l, 8);
+        l += __shfl_xor_sync(kFull, l, 16);
+        const int h = 8 * t + 2 * c + e;
+        if (r == 0) {
+          row_ml[2 * h] = s.m10[t][e];
+          row_ml[2 * h + 1] = l;
+        }
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          const float bias = __shfl_sync(kFull, s.bacc[t][e], g * 4 + c);
+          const float fe = p2(s.E[g]);
+#pragma unroll
+          for (int j = g * GS / DB; j < (g + 1) * GS / DB; j++) {
+            constexpr float f1 = (float)(1 << (24 - BITS));
+            if constexpr (BITS == 4) {
+              float4 v;
+              v.x = fmaf(s.acc[2 * j][t][e], f1, bias) * fe;
+              v.y = fmaf(s.acc[2 * j][t][e + 2], f1 / 16, bias) * fe;
+              v.z = fmaf(s.acc[2 * j + 1][t][e], f1, bias) * fe;
+              v.w = fmaf(s.acc[2 * j + 1][t][e + 2], f1 / 16, bias) * fe;
+              *reinterpret_cast<float4 *>(row_o + h * SROW + 32 * j + 4 * r) = v;
+            } else {
+              float2 v;
+              v.x = fmaf(s.acc[j][t][e], f1, bias) * fe;
+              v.y = fmaf(s.acc[j][t][e + 2], f1, bias) * fe;
+              *reinterpret_cast<float2 *>(row_o + h * SROW + 16 * j + 2 * r) = v;
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+// Rounds and stores one output element.
+__device__ __forceinline__ void store_out(const Args &a, int64_t i, float v) {
+  a.out[i] = a.f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+// log-sum-exp (natural) from the scaled max and total.
+__device__ __forceinline__ float lse_of(float m10, float l) {
+  return l > 0.0f ? (m10 + log2f(l)) * 0.6931471805599453f : (l == 0.0f ? -INFINITY : l);
+}
+
+template <int BITS, int D, int GS, int NT, bool PREC>
+__global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
+  using K = Kernel<BITS, D, GS, NT, PREC>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t bars[kWarps * 8];
+  __shared__ Start start;
+  __shared__ long long scan[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  float *join = reinterpret_cast<float *>(smem_raw);                         // [warp][GHP][SROW], then [warp][GHP][2]
+  float *join_ml = join + kWarps * K::GHP * K::SROW;
+  unsigned char *ring = smem_raw + ((K::kJoin + 15) & ~15) + warp * a.depth * K::GB;
+  uint64_t *bar = bars + warp * 8;
+
+  if (lane == 0)
+    for (int i = 0; i < a.depth; i++) mbar_init(bar + i, 1);
+  fence_mbar_init();
+  pdl_launch_dependents();
+  pdl_wait();
+  find_start(a, &start, scan);   // (its barriers also publish the mbarriers)
+
+  // rows without a token: zeros, and minus infinity for the log-sum-exp
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (granules(a, b, false) == 0) {
+      const int64_t row = (int64_t)b * a.H * a.G;
+      for (int i = tid; i < a.H * a.G * D; i += kThreads) a.out[row * D + i] = 0;
+      if (a.lse)
+        for (int i = tid; i < a.H * a.G; i += kThreads) a.lse[row + i] = -INFINITY;
+    }
+  constexpr int kPart = Ws<D, K::GHP>::kPart;
+  Rec *recs = reinterpret_cast<Rec *>(a.ws + (int64_t)2 * gridDim.x * kPart);
+  const long long mine = min(start.per, start.total - start.first);
+  if (mine <= 0 || start.b >= a.B) {
+    if (tid == 0) recs[blockIdx.x] = Rec{0, 0, 0, 0};
+    return;
+  }
+  // piece walked by the whole CTA (pc) and the copies of this warp (cp), ahead of it
+  Cursor cp{}, pc{};
+  cp.b = pc.b = start.b;
+  cp.hc = pc.hc = start.hc;
+  cp.left = pc.left = mine;
+  cursor_open(a, pc, start.g, 0);
+  cursor_open(a, cp, start.g, warp);
+  cursor_settle(a, cp, warp);
+  if (tid == 0) recs[blockIdx.x] = Rec{start.b, start.hc, start.g, pc.n};
+
+  uint32_t filled = 0, phase = 0;     // slots with a copy, parity of each slot's next wait
+  int slot_in = 0, slot_out = 0;
+  bool dead = false;
+  auto issue = [&]() {                // the cursor's granule into slot_in
+    if (cp.g >= cp.end) return;
+    const int page = cp.page;
+    if (page >= 0 && page < a.pages) {
+      if (lane == 0) {
+        const int64_t off = (((int64_t)page * a.H + cp.hc / a.chunks) << a.gshift) + (cp.g & ((1 << a.gshift) - 1));
+        mbar_arrive_expect_tx(bar + slot_in, K::GB);
+        bulk_load(ring + slot_in * K::GB, a.cache + off * K::GB, K::GB, bar + slot_in);
+      }
+      filled |= 1u << slot_in;
+    } else if (lane == 0) {
+      atomicOr(&g_device_error, kErrIndex);      // the granule is left out
+    }
+    slot_in = slot_in + 1 == a.depth ? 0 : slot_in + 1;
+    cp.g += kWarps;
+    cursor_page(a, cp);
+    cursor_settle(a, cp, warp);
+  };
+  for (int i = 0; i < a.depth; i++) issue();
+
+  typename K::State s;
+  int g_first = start.g;
+  bool first_piece = true;
+  while (true) {
+    // ---- this piece's queries: chunk of heads [h0, h0 + heads) of kv head pc.hc / chunks
+    const int chunk = pc.hc % a.chunks;
+    const int h0 = (pc.hc / a.chunks) * a.G + chunk * a.GH;
+    const int heads = min(a.GH, a.G - chunk * a.GH);
+    uint32_t qf[K::KM][NT][2];
+    float qsum[K::NG][NT][2], sf[NT][2];
+    const uint16_t *q = a.q + (int64_t)pc.b * a.q_stride;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      // lane r holds head 8t + r; its elements in the order of the score MMAs
+      const bool in = 8 * t + r < heads;
+      const uint16_t *row = q + (int64_t)(h0 + (in ? 8 * t + r : 0)) * D;
+      float v[D / 4], mx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 32; i++) {
+        // 4-bit: word 4i + c covers elements 32i + 8c ..+7; 8-bit: words 8i + c and 8i + 4 + c, four each
+        uint32_t p[4];
+        if constexpr (BITS == 4) {
+          *reinterpret_cast<uint4 *>(p) = __ldg(reinterpret_cast<const uint4 *>(row + 32 * i + 8 * c));
+        } else {
+          *reinterpret_cast<uint2 *>(p) = __ldg(reinterpret_cast<const uint2 *>(row + 32 * i + 4 * c));
+          *reinterpret_cast<uint2 *>(p + 2) = __ldg(reinterpret_cast<const uint2 *>(row + 32 * i + 16 + 4 * c));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const uint16_t hb = (uint16_t)(p[e / 2] >> (e % 2 * 16));
+          v[8 * i + e] = in ? q_at(&hb, a.f16) : 0.0f;
+          mx = fmaxf(mx, fabsf(v[8 * i + e]));
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+      // q * 2^up has its largest element in [2^12, 2^13)
+      const int up = min(120, max(-120, 139 - (int)(__float_as_uint(mx) >> 23)));
+      const float fu = pow2f(up);
+      float part[K::NG];
+#pragma unroll
+      for (int g = 0; g < K::NG; g++) part[g] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 32; i++) {
+        float *x = v + 8 * i;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          x[e] *= fu;
+          const int g = (BITS == 4 ? 32 * i : 32 * i + 16 * (e / 4)) / GS;
+          part[g] += x[e];
+        }
+        if constexpr (BITS == 4) {
+          qf[2 * i][t][0] = pack_h2(x[0], x[4]);
+          qf[2 * i][t][1] = pack_h2(x[1] * 0.0625f, x[5] * 0.0625f);
+          qf[2 * i + 1][t][0] = pack_h2(x[2], x[6]);
+          qf[2 * i + 1][t][1] = pack_h2(x[3] * 0.0625f, x[7] * 0.0625f);
+        } else {
+          qf[2 * i][t][0] = pack_h2(x[0], x[2]);
+          qf[2 * i][t][1] = pack_h2(x[1], x[3]);
+          qf[2 * i + 1][t][0] = pack_h2(x[4], x[6]);
+          qf[2 * i + 1][t][1] = pack_h2(x[5], x[7]);
+        }
+      }
+      // per-head constants for the score fragment's columns 2c, 2c + 1
+      const float back = a.scale_log2 * pow2f(24 - up < -126 ? -126 : (24 - up > 127 ? 127 : 24 - up));
+#pragma unroll
+      for (int g = 0; g < K::NG; g++) {
+        part[g] += __shfl_xor_sync(kFull, part[g], 1);
+        part[g] += __shfl_xor_sync(kFull, part[g], 2);
+        part[g] *= 0x1p-24f;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const int src = (2 * c + e) * 4;
+        sf[t][e] = __shfl_sync(kFull, back, src);
+#pragma unroll
+        for (int g = 0; g < K::NG; g++) qsum[g][t][e] = __shfl_sync(kFull, part[g], src);
+      }
+    }
+    K::reset(s);
+    const int len = min(max(0, __ldg(a.lens + pc.b)), a.cap_gran * kv::kTok);
+
+    // ---- this warp's granules of the piece
+    for (int g = g_first + warp; g < pc.end; g += kWarps) {
+      if ((filled >> slot_out & 1u) && !dead) {
+        if (mbar_wait(bar + slot_out, phase >> slot_out & 1u)) {
+          K::granule(ring + slot_out * K::GB, len - g * kv::kTok, qf, qsum, sf, s);
+          phase ^= 1u << slot_out;
+          filled &= ~(1u << slot_out);
+        } else {
+          dead = true;
+        }
+      }
+      __syncwarp();
+      slot_out = slot_out + 1 == a.depth ? 0 : slot_out + 1;
+      if (!dead) issue();
+    }
+
+    // ---- join the warps: row h of every warp's sums, scaled to the common max
+    K::to_join(s, join + warp * K::GHP * K::SROW, join_ml + warp * K::GHP * 2);
+    __syncthreads();
+    const bool whole = g_first == 0 && pc.end == pc.n;
+    const int64_t part_id = (int64_t)blockIdx.x * 2 + (first_piece && g_first > 0 ? 0 : 1);
+    float *part = a.ws + part_id * kPart;
+    for (int i = tid; i < heads * (D / 4); i += kThreads) {
+      const int h = i / (D / 4), d = i % (D / 4) * 4;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; w++)
+        if (join_ml[(w * K::GHP + h) * 2 + 1] != 0.0f) m = fmaxf(m, join_ml[(w * K::GHP + h) * 2]);
+      float l = 0.0f;
+      float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        const float lw = join_ml[(w * K::GHP + h) * 2 + 1];
+        if (lw == 0.0f) continue;                      // a warp without a granule
+        const float f = ex2(join_ml[(w * K::GHP + h) * 2] - m);
+        const float4 v = *reinterpret_cast<const float4 *>(join + (w * K::GHP + h) * K::SROW + d);
+        l = fmaf(lw, f, l);
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+      }
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t row = (int64_t)pc.b * a.H * a.G + h0 + h;
+        store_out(a, row * D + d, o.x * inv);
+        store_out(a, row * D + d + 1, o.y * inv);
+        store_out(a, row * D + d + 2, o.z * inv);
+        store_out(a, row * D + d + 3, o.w * inv);
+        if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
+      } else {
+        *reinterpret_cast<float4 *>(part + h * D + d) = o;
+        if (d == 0) {
+          part[K::GHP * D + 2 * h] = m;
+          part[K::GHP * D + 2 * h + 1] = l;
+        }
+      }
+    }
+    if (pc.left <= 0) break;
+    cursor_next_piece(a, pc, 0);
+    if (pc.end == 0) break;
+    first_piece = false;
+    g_first = 0;
+    __syncthreads();
+  }
+  // copies still in flight (only after a wait gave up) land before the CTA's memory is freed
+  if (dead)
+    for (int i = 0; i < a.depth; i++)
+      if (filled >> i & 1u) mbar_wait(bar + i, phase >> i & 1u);
+}
+
+// Joins the pieces of a (sequence, head chunk) that shares cut.  Block i looks at
+// the boundary in front of share i: if it is the first one inside its pair, the
+// block adds the piece that ends share i - 1 and those that begin share i, i + 1, ...
+template <int D, int GHP>
+__global__ void __launch_bounds__(kThreads) k_attn_join(const Args a, int ctas) {
+  constexpr int kPart = Ws<D, GHP>::kPart;
+  pdl_launch_dependents();
+  pdl_wait();
+  const Rec *recs = reinterpret_cast<const Rec *>(a.ws + (int64_t)2 * ctas * kPart);
+  const int i = blockIdx.x + 1;
+  // (read through L2: nothing of the workspace may come from an earlier launch's lines in L1)
+  auto rec_at = [&](int j) {
+    const int4 v = __ldcg(reinterpret_cast<const int4 *>(recs + j));
+    return Rec{v.x, v.y, v.z, v.w};
+  };
+  const Rec rec = rec_at(i);
+  if (rec.n == 0 || rec.g0 == 0) return;
+  const Rec prev = rec_at(i - 1);
+  if (prev.b == rec.b && prev.hc == rec.hc && prev.g0 > 0) return;   // an earlier boundary is inside this pair
+  int last = i;                                                      // shares that begin inside the pair
+  while (last + 1 < ctas) {
+    const Rec nx = rec_at(last + 1);
+    if (nx.n == 0 || nx.b != rec.b || nx.hc != rec.hc || nx.g0 == 0) break;
+    last++;
+  }
+  const int chunk = rec.hc % a.chunks;
+  const int h0 = (rec.hc / a.chunks) * a.G + chunk * a.GH;
+  const int heads = min(a.GH, a.G - chunk * a.GH);
+  // piece j = 0: end of share i - 1; j > 0: beginning of share i + j - 1
+  auto part = [&](int j) { return a.ws + (int64_t)(j == 0 ? 2 * (i - 1) + 1 : 2 * (i + j - 1)) * kPart; };
+  const int pieces = last - i + 2;
+  for (int e = threadIdx.x; e < heads * (D / 4); e += kThreads) {
+    const int h = e / (D / 4), d = e % (D / 4) * 4;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int j = 0; j < pieces; j++) {
+      const float *p = part(j);
+      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + GHP * D + 2 * h));
+      const float mj = ml.x, lj = ml.y;
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + h * D + d));
+      if (lj == 0.0f) continue;
+      const float mn = fmaxf(m, mj);
+      const float fo = ex2(m - mn), fj = ex2(mj - mn);
+      m = mn;
+      l = fmaf(lj, fj, l * fo);
+      o.x = fmaf(v.x, fj, o.x * fo);
+      o.y = fmaf(v.y, fj, o.y * fo);
+      o.z = fmaf(v.z, fj, o.z * fo);
+      o.w = fmaf(v.w, fj, o.w * fo);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t row = (int64_t)rec.b * a.H * a.G + h0 + h;
+    store_out(a, row * D + d, o.x * inv);
+    store_out(a, row * D + d + 1, o.y * inv);
+    store_out(a, row * D + d + 2, o.z * inv);
+    store_out(a, row * D + d + 3, o.w * inv);
+    if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
+  }
+}
+
+}  // namespace attn
+}  // namespace
+}  // namespace gwb
+
+namespace gwb {
+namespace {
+
+attn::Args attn_args(const AttnCall &c) {
+  attn::Args a{};
+  a.q = c.q; a.q_stride = c.q_stride;
+  a.cache = static_cast<const unsigned char *>(c.cache.data);
+  a.table = c.table; a.table_stride = c.table_stride;
+  a.lens = c.lens;
+  a.out = c.out; a.lse = c.lse;
+  a.ws = static_cast<float *>(c.ws);
+  a.pages = c.cache.pages;
+  a.B = (int)c.B; a.H = (int)c.cache.heads; a.G = (int)(c.q_heads / c.cache.heads);
+  a.chunks = (a.G + 8 * c.tiles - 1) / (8 * c.tiles);
+  a.GH = (a.G + a.chunks - 1) / a.chunks;
+  int gpp = (int)(c.cache.page_size / kv::kTok);
+  while (gpp >>= 1) a.gshift++;
+  const int64_t cap = c.max_pages * (c.cache.page_size / kv::kTok);
+  a.cap_gran = (int)(cap < (1 << 27) ? cap : (1 << 27) - 1);   // (16 times this stays an int)
+  a.min_per = attn::kWarps;
+  a.f16 = c.f16;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  return a;
+}
+
+// Launches of one instance: the attention, then the join that depends on it.
+template <int BITS, int D, int GS, int NT, bool PREC>
+gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
+  using K = attn::Kernel<BITS, D, GS, NT, PREC>;
+  auto kern = attn::k_attn_decode<BITS, D, GS, NT, PREC>;
+  const size_t join = (K::kJoin + 15) & ~15;
+  // ring depth: what lets four CTAs share an SM (227 KB less 1 KB a CTA), at least 2 slots, at most 6
+  int depth = (int)((227 * 1024 / 4 - 1536 - join) / ((size_t)attn::kWarps * K::GB));
+  depth = join + 1536 > 227 * 1024 / 4 ? 2 : (depth < 2 ? 2 : (depth > 6 ? 6 : depth));
+  const size_t smem = join + (size_t)attn::kWarps * depth * K::GB;
+  AttnSetup su;
+  gwb_status s = attn_setup(reinterpret_cast<const void *>(kern), smem, attn::kThreads, &su);
+  if (s != GWB_OK) return s;
+  const int ctas = su.sms * (su.per_sm < kAttnMaxPerSm ? su.per_sm : kAttnMaxPerSm);
+  const int64_t need = (int64_t)ctas * (2 * 4 * attn::Ws<D, K::GHP>::kPart + (int64_t)sizeof(attn::Rec));
+  if (ws_bytes < need)
+    return fail(GWB_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  a.depth = depth;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(attn::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
+  cfg.gridDim = dim3((unsigned)(ctas - 1));
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, attn::k_attn_join<D, K::GHP>, a, ctas);
+  if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode join launch: %s", cudaGetErrorString(e));
+  return GWB_OK;
+}
+
+}  // namespace
+}  // namespace gwb

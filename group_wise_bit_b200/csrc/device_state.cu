@@ -12,7 +12,7 @@
 namespace gwb {
 namespace {
 
-constexpr int kMaxUnits = 16;
+constexpr int kMaxUnits = 32;
 
 std::vector<DeviceStateAddrs> &registry() {
   static std::vector<DeviceStateAddrs> r;   // filled while the library loads

@@ -39,6 +39,51 @@ void launch_quant_per_token_i8(const uint16_t *x, int64_t M, int64_t K, int8_t *
 void launch_qpack_sym_i8(const float *w, int64_t N, int64_t K, int8_t *wq, float *sw, cudaStream_t st);
 void launch_qpack_sym_i4(const float *w, int64_t N, int64_t K, uint32_t *wq, float *sw, cudaStream_t st);
 
+// ------------------------------------------------------------ norm, key-value cache, decode attention
+void launch_rmsnorm_quant_i8(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, int64_t M,
+                             int64_t K, double eps, bool f16, uint16_t *residual_out, int8_t *qx, float *sx,
+                             cudaStream_t st);
+// A paged, quantized cache (kv_layout.cuh).
+struct KvCache {
+  void *data;
+  int64_t pages, heads, page_size;
+  int head_dim, bits, gs;
+};
+int64_t kv_granule_bytes(int head_dim, int bits, int gs);
+void launch_kv_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride, const int64_t *slots,
+                     int64_t T, const KvCache &c, bool f16, cudaStream_t st);
+void launch_kv_read(const KvCache &c, const int64_t *slots, int64_t T, uint16_t *k, uint16_t *v, bool f16,
+                    cudaStream_t st);
+struct AttnCall {
+  const uint16_t *q;
+  int64_t q_stride, B, q_heads;
+  KvCache cache;
+  const int32_t *table;
+  int64_t table_stride, max_pages;
+  const int32_t *lens;
+  float scale;
+  bool f16;
+  uint16_t *out;
+  float *lse;
+  void *ws;
+  int64_t ws_bytes;
+  int tiles;                    // 8-head tiles of a CTA's chunk
+};
+constexpr int kAttnMaxPerSm = 4;
+// SMs of the current device and resident CTAs of a kernel with `smem` bytes of
+// dynamic shared memory (whose attribute is set), looked up once a kernel and device.
+struct AttnSetup {
+  int sms, per_sm;
+};
+gwb_status attn_setup(const void *kern, size_t smem, int threads, AttnSetup *out);
+int attn_tiles(int64_t group, int head_dim);
+gwb_status attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, int64_t *bytes);
+gwb_status launch_attn_decode(AttnCall c, cudaStream_t st);
+gwb_status launch_attn_4_bf16(const AttnCall &c, cudaStream_t st);
+gwb_status launch_attn_4_fp16(const AttnCall &c, cudaStream_t st);
+gwb_status launch_attn_8_bf16(const AttnCall &c, cudaStream_t st);
+gwb_status launch_attn_8_fp16(const AttnCall &c, cudaStream_t st);
+
 // ------------------------------------------------------------ GEMV regime (M <= 8)
 // Returns false when the (bits, gs) combination has no GEMV kernel (the caller
 // then uses the tensor-core path).

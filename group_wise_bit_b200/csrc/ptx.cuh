@@ -10,12 +10,14 @@
 
 namespace gwb {
 
-// Device error flag (bit 0: a bounded wait gave up) and the wait limit in
+// Device error flag (bit 0: a bounded wait gave up; bit 1: an index given in
+// device memory was out of range and was left out) and the wait limit in
 // clock cycles (kWaitCycles unless a test lowered it).  Device code is compiled
 // per translation unit, so each unit that includes this header has its own
 // copy of both; every unit registers them (below), and the host reads and
 // clears all flags in one step and sets all limits together (device_state.cu).
 constexpr unsigned long long kWaitCycles = 4000000000ull;  // ~2 s at 1.9 GHz
+constexpr unsigned int kErrTimeout = 1u, kErrIndex = 2u;
 static __device__ unsigned int g_device_error = 0;
 static __device__ unsigned long long g_wait_cycles = kWaitCycles;
 
@@ -92,7 +94,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
   const unsigned long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (clock64() - t0 > limit) {
-      atomicOr(&g_device_error, 1u);
+      atomicOr(&g_device_error, kErrTimeout);
       return false;
     }
   }

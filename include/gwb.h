@@ -72,6 +72,9 @@ typedef enum gwb_status {
     GWB_ERR_TIMEOUT = 6       /* a bounded device-side wait gave up                      */
 } gwb_status;
 
+/* Element type of activations where an entry point takes either. */
+typedef enum gwb_dtype { GWB_BF16 = 0, GWB_F16 = 1 } gwb_dtype;
+
 /* Message for the calling thread's most recent non-GWB_OK return ("" if none).
  * The string is owned by the library and valid until the next call on this thread. */
 const char *gwb_last_error(void);
@@ -83,7 +86,10 @@ const char *gwb_version(void);
  * flag, which every bounded wait of the library's kernels sets when it gives
  * up (one flag per device, shared by all kernels).  Returns GWB_OK when no wait
  * gave up since the last check, GWB_ERR_TIMEOUT otherwise, GWB_ERR_CUDA when
- * the synchronization itself failed.  A kernel whose wait gave up stops
+ * the synchronization itself failed.  The cache entry points report a slot,
+ * page id or length in device memory that was out of range the same way, as
+ * GWB_ERR_INVALID_ARG (what it named was left out; nothing outside the given
+ * tensors is read or written).  A kernel whose wait gave up stops
  * issuing work, lets the copies it started land, frees its tensor memory and
  * returns, so the context stays usable; its outputs are then undefined.
  * Source: metrale_gpu_runtime/mlx_int8.rs, MlxInt8Weight::load (failures are
@@ -329,6 +335,94 @@ gwb_status gwb_qpack_sym_i8(const float *w, int64_t N, int64_t K, int8_t *wq, fl
 gwb_status gwb_gemm_i8i8(const int8_t *qx, const float *sx, int64_t M, const int8_t *wq,
                          const float *sw, int64_t N, int64_t K, uint16_t *y, int32_t *acc,
                          void *stream);
+
+/* ------------------------------------------------------------------ norm with an int8 output */
+
+/* rmsnorm_quant_i8 -- root-mean-square norm with the residual's addition, and
+ * the dynamic per-token int8 activations of gwb_gemm_i8i8 / gwb_gemm_i8i4 as its
+ * output:
+ *   h  = residual ? round(x + residual) : x        (rounded once to `dtype`; stored)
+ *   r  = fp32(1 / sqrt(mean_k h[m,k]^2 + eps))     (sum and root in fp64)
+ *   y  = (h * r) * weight                          (fp32, one rounding a product; not stored)
+ *   sx[m] = max_k |y| / 127;  qx[m,k] = clip(round_half_even(y / sx[m]), -127, 127)
+ * (0 when the row of y is zero).  The quantizer is gwb_quant_per_token_i8's, on
+ * the fp32 norm instead of a rounded copy of it.
+ *   x, residual  bf16 / fp16 [M, K] (finite; residual NULL or given together with residual_out)
+ *   weight       bf16 / fp16 [K]
+ *   residual_out [M, K] h, may be x or residual themselves
+ *   qx int8 [M, K], sx fp32 [M]
+ * dtype: a gwb_dtype.  eps >= 0.  Any K; multiples of 8 use 16-byte accesses. */
+gwb_status gwb_rmsnorm_quant_i8(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
+                                int64_t M, int64_t K, double eps, int dtype, uint16_t *residual_out,
+                                int8_t *qx, float *sx, void *stream);
+
+/* ------------------------------------------------------------------ quantized paged cache
+ * Keys and values of past tokens, quantized group-wise in the MLX affine scheme
+ * (gwb_qpack_affine's arithmetic along the head dimension) and kept in pages.
+ *
+ * cache: uint8 [pages, heads, block], block = gwb_kv_block_bytes().  A slot is
+ * page * page_size + place in the page.  A block is page_size / 16 granules of
+ * 16 tokens, each, with NW = head_dim*bits/32 words a row, NG groups, VW = min(4, NW/4):
+ *   key codes    u32 [NW/(4 VW)][16][4][VW]      word 4(VW a + v) + c of token t at [a][rho(t)][c][v],
+ *                                                rho(t) = 2(t/4) + t%2 + 8(t/2%2)
+ *   value codes  u16 [NW/8][8][4][2][2][2]       half 16a + 8j + r of token 4c + 2y + z at [a][r][c][j][y][z]
+ *   key meta     bf16 [16][NG][2]                scale and bias of row rho(t)
+ *   value meta   bf16 [NG][16], bf16 [NG][16]    scales, then biases, of token t
+ * where words and halves are those of the token's MLX-packed row (lowest bits =
+ * lowest column).  The order is the one the decode attention takes its tensor-core
+ * operands in.
+ * bits in {4, 8}; head_dim in {64, 128, 256}; group_size in {32, 64, 128}, a
+ * divisor of head_dim; page_size a power of two from 16 to 4096.  Rows of k, v
+ * and q are bf16 or fp16 (`dtype`), 16-byte aligned, heads contiguous, tokens
+ * `stride` elements apart (a multiple of 8), so slices of a fused projection
+ * need no copy. */
+
+/* Bytes of one page of one head. */
+gwb_status gwb_kv_block_bytes(int64_t page_size, int head_dim, int bits, int group_size, int64_t *bytes);
+
+/* kv_write -- quantizes T tokens' keys and values into their slots.
+ *   k, v   [T, heads, head_dim] (finite), tokens k_stride / v_stride elements apart
+ *   slots  int64 [T] on the device; a negative slot is a padded row, which is
+ *          left out, and so is one beyond the cache (see gwb_check_device_error).
+ * Slots must be distinct: a slot named twice holds a mixture of its rows
+ * afterwards.  Codes, scales and biases are bit-exact (gwb_qpack_affine's). */
+gwb_status gwb_kv_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                        const int64_t *slots, int64_t T, int dtype, void *cache, int64_t pages,
+                        int64_t heads, int64_t page_size, int head_dim, int bits, int group_size,
+                        void *stream);
+
+/* kv_read -- the rows at `slots` (int64 [T], any order, repeats allowed) as
+ * dense bf16 / fp16 k, v [T, heads, head_dim]: round(fp32(code*scale + bias)).
+ * A negative slot, or one beyond the cache, gives a row of zeros. */
+gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t page_size, int head_dim,
+                       int bits, int group_size, const int64_t *slots, int64_t T, int dtype,
+                       uint16_t *k, uint16_t *v, void *stream);
+
+/* ------------------------------------------------------------------ decode attention
+ * attn_decode -- attention of one new token a sequence over the quantized cache:
+ *   out[b,h] = sum_t p[t] v[t] / sum_t p[t],  p[t] = exp(scale * q[b,h] . k[t]),  t < seq_lens[b]
+ * with k, v the values the cache's codes stand for, query head h reading kv
+ * head h / (q_heads / heads).
+ *   q           [B, q_heads, head_dim], sequences q_stride elements apart
+ *   page_table  int32 [B, max_pages], rows table_stride apart: page ids of the sequence's tokens
+ *   seq_lens    int32 [B]; 0 (or less) is an empty row: zeros, lse = -inf
+ *   out         [B, q_heads, head_dim], dense, of q's dtype
+ *   lse         fp32 [B, q_heads] or NULL: log of sum_t p[t] (natural logarithm)
+ *   workspace   gwb_attn_decode_workspace() bytes, contents irrelevant before and after; calls that
+ *               may overlap on the GPU need one each
+ * Lengths are read on the device only, so a captured graph follows them.  A
+ * length beyond max_pages * page_size is cut to it, and the 16 tokens of a
+ * granule whose page id is outside the cache are left out; both are reported
+ * by gwb_check_device_error.  Scores, sums and the softmax are fp32; keys, values
+ * and q enter exactly, the softmax weights as fp16 (with bf16 outputs) or as
+ * fp16 pairs (with fp16 outputs).  Deterministic for given lengths and device. */
+gwb_status gwb_attn_decode_workspace(int64_t q_heads, int64_t heads, int head_dim, int64_t *bytes);
+gwb_status gwb_attn_decode(const uint16_t *q, int64_t q_stride, int64_t B, int64_t q_heads, int dtype,
+                           const void *cache, int64_t pages, int64_t heads, int64_t page_size,
+                           int head_dim, int bits, int group_size, const int32_t *page_table,
+                           int64_t table_stride, int64_t max_pages, const int32_t *seq_lens, float scale,
+                           uint16_t *out, float *lse, void *workspace, int64_t workspace_bytes,
+                           void *stream);
 
 #ifdef __cplusplus
 }
