@@ -128,11 +128,18 @@ __device__ __forceinline__ float q_at(const uint16_t *p, int f16) {
   return f16 ? __half2float(__ushort_as_half(*p)) : __uint_as_float((uint32_t)*p << 16);
 }
 
-// Where the share of a CTA begins: sequence, head chunk and granule, and the
-// share size.  Every thread sums a run of the lengths, one warp scan joins them.
+// The line of work.  A pair (sequence, head chunk) of n granules takes
+// kPieceCost + n units: opening a piece (staging q, joining the warps) costs
+// about as much as kPieceCost granules do, so shares of many short sequences
+// stay level with shares of long ones.  A share that begins inside a pair's first
+// kPieceCost units begins at its granule 0; one that ends there leaves the pair
+// to the next share.
+constexpr int kPieceCost = 8;
+
+// Where the share of a CTA begins, and its length.
 struct Start {
-  int b, hc, g, pad;
-  long long per, total, first;   // granules a share, of the whole line, before this CTA
+  int b, hc, u, pad;             // sequence, head chunk and unit in the pair
+  long long left;                // units of the share; 0: nothing to do
 };
 
 __device__ __forceinline__ int granules(const Args &a, int b, bool report) {
@@ -144,13 +151,15 @@ __device__ __forceinline__ int granules(const Args &a, int b, bool report) {
   }
   return n;
 }
+__device__ __forceinline__ long long units(int n) { return n > 0 ? n + kPieceCost : 0; }
 
+// Every thread sums a run of the lengths, a scan joins them.
 __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *scan) {
   const int tid = threadIdx.x, HC = a.H * a.chunks;
   const int run = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
   long long mine = 0;
-  for (int b = b0; b < b1; b++) mine += granules(a, b, blockIdx.x == 0);
+  for (int b = b0; b < b1; b++) mine += units(granules(a, b, blockIdx.x == 0));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -158,6 +167,7 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
     if ((tid & 31) >= o) inc += t;
   }
   if ((tid & 31) == 31) scan[tid >> 5] = inc;
+  if (tid == 0) st->left = 0;
   __syncthreads();
   long long before = inc - mine, total = 0;
 #pragma unroll
@@ -169,21 +179,15 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
   total *= HC;
   const long long per = max((long long)a.min_per, (total + gridDim.x - 1) / gridDim.x);
   const long long first = per * blockIdx.x;
-  if (tid == 0) {
-    st->per = per;
-    st->total = total;
-    st->first = first;
-    st->b = a.B;
-  }
-  __syncthreads();
-  if (first < total && mine > 0 && first >= before && first < before + mine * HC) {
+  if (first < total && first >= before && first < before + mine * HC) {
     long long left = first - before;
     for (int b = b0; b < b1; b++) {
-      const long long n = granules(a, b, false);
+      const long long n = units(granules(a, b, false));
       if (left < n * HC) {
         st->b = b;
         st->hc = (int)(left / n);
-        st->g = (int)(left - (long long)st->hc * n);
+        st->u = (int)(left - (long long)st->hc * n);
+        st->left = min(per, total - first);
         break;
       }
       left -= n * HC;
@@ -192,47 +196,57 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
   __syncthreads();
 }
 
-// The stream of granules one warp copies: within a piece every kWarps-th, then
-// the next piece of the CTA's share.
+// A walk over the pieces of a share.  The CTA has one (step 1); each warp has
+// one for its copies, which takes every kWarps-th granule of a piece.
 struct Cursor {
-  int b, hc, g, end;            // current piece; granules [g, end) are left to this warp
-  long long left;               // granules of the share behind this piece
-  int n;                        // granules of sequence b
+  int b, hc, n;                 // pair, granules of the sequence
+  int g, end;                   // granules [g, end) of the piece are left to this walker
+  long long left;               // units of the share behind this piece
+  const unsigned char *head;    // the pair's head in page 0
+  const int32_t *row;           // the sequence's page ids
   int page;                     // page id of granule g (loaded one granule ahead)
 };
 
 __device__ __forceinline__ void cursor_page(const Args &a, Cursor &c) {
-  if (c.g < c.end) c.page = __ldg(a.table + (int64_t)c.b * a.table_stride + (c.g >> a.gshift));
+  if (c.g < c.end) c.page = __ldg(c.row + (c.g >> a.gshift));
 }
-// Opens the piece that starts at granule g of (b, hc), skipping empty sequences.
-__device__ __forceinline__ void cursor_open(const Args &a, Cursor &c, int g, int warp) {
-  while (c.left > 0) {
-    if (c.b >= a.B) { c.left = 0; break; }
+// Opens the piece at unit u of (b, hc), skipping empty sequences; false when the share ends in front of it.
+template <int GB>
+__device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int first) {
+  c.g = c.end = 0;
+  while (c.left > 0 && c.b < a.B) {
     c.n = granules(a, c.b, false);
     if (c.n > 0) {
+      const int g = max(0, u - kPieceCost);
+      c.left -= max(0, kPieceCost - u);
       const int len = (int)min((long long)(c.n - g), c.left);
+      if (len <= 0) break;
       c.left -= len;
       c.end = g + len;
-      c.g = g + warp;
+      c.g = g + first;
+      c.head = a.cache + (((int64_t)(c.hc / a.chunks)) << a.gshift) * GB;
+      c.row = a.table + (int64_t)c.b * a.table_stride;
       cursor_page(a, c);
-      return;
+      return true;
     }
     c.b++;
     c.hc = 0;
   }
-  c.g = c.end = 0;
+  c.left = 0;
+  return false;
 }
-__device__ __forceinline__ void cursor_next_piece(const Args &a, Cursor &c, int warp) {
-  if (c.left <= 0) { c.g = c.end = 0; return; }
+template <int GB>
+__device__ __forceinline__ bool cursor_next_piece(const Args &a, Cursor &c, int first) {
   if (++c.hc == a.H * a.chunks) {
     c.hc = 0;
     c.b++;
   }
-  cursor_open(a, c, 0, warp);
+  return cursor_open<GB>(a, c, 0, first);
 }
-// Leaves the cursor on a granule of this warp, or at the end (g == end, left == 0).
-__device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int warp) {
-  while (c.g >= c.end && c.left > 0) cursor_next_piece(a, c, warp);
+// Leaves a warp's cursor on a granule of its own, or at the end (g >= end, left == 0).
+template <int GB>
+__device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int first) {
+  while (c.g >= c.end && c.left > 0) cursor_next_piece<GB>(a, c, first);
 }
 
 template <int BITS, int D, int GS, int NT, bool PREC>
@@ -253,8 +267,22 @@ struct Kernel {
     float acc[VB * MPB][NT][4];
     float bacc[NT][4];            // row r < NG: sum of P * (bias + Z scale) of group r
     float m10[NT][2], l[NT][2];   // running max (log2, minus kLogP) and this lane's total, heads 8 nt + 2c, +1
-    int E[NG];                    // value scales and biases are held over 2^E
+    int E[NG];                    // value scales and biases are held over 2^E ...
+    float fs[NG];                 // ... and this is 2^(BITS - E)
+    float fb;                     // 2^-E of this lane's group r % NG, and the largest scale and |bias|
+    uint32_t lim_s, lim_b;        // (bf16 bits) that 2^E holds
   };
+
+  // Scale bits below 2^(E - BITS) and |bias| bits below 2^E fit.
+  static __device__ __forceinline__ void set_exponent(State &s, int g, int e, bool own) {
+    s.E[g] = e;
+    s.fs[g] = p2(BITS - e);
+    if (own) {
+      s.fb = p2(-e);
+      s.lim_s = (uint32_t)(max(0, 127 + e - BITS) << 7) - 1u;
+      s.lim_b = (uint32_t)((127 + e) << 7) - 1u;
+    }
+  }
 
   static __device__ __forceinline__ void reset(State &s) {
 #pragma unroll
@@ -271,7 +299,17 @@ struct Kernel {
       s.l[t][0] = s.l[t][1] = 0.0f;
     }
 #pragma unroll
-    for (int g = 0; g < NG; g++) s.E[g] = -100;
+    for (int g = 0; g < NG; g++) set_exponent(s, g, -100, g == ((threadIdx.x & 31) >> 2) % NG);
+  }
+
+  // Zeroes the value scales and biases behind the length (the cache may hold
+  // anything there, and 0 * NaN is NaN), before the slot's next copy by a fence.
+  static __device__ __forceinline__ void clear_tail(unsigned char *sm, int valid) {
+    uint16_t *meta = reinterpret_cast<uint16_t *>(sm + 2 * L.code_bytes + 64 * NG);
+    for (int i = threadIdx.x & 31; i < 2 * NG * 16; i += 32)
+      if (i % 16 >= valid) meta[i] = 0;
+    fence_proxy_async_smem();
+    __syncwarp();
   }
 
   // One granule: scores, running max, P, values.  `valid`: its tokens in front of the length.
@@ -354,17 +392,22 @@ struct Kernel {
       }
     }
     // ---- running max: moved only when a P would pass 2^14
-    const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8
-    const bool in0 = t0 < valid, in1 = t0 + 2 < valid;
     float y[NT][4], top = -INFINITY;
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        y[t][j] = (j < 2 ? in0 : in1) ? fmaf(sc[t][j], sf[t][j & 1], -s.m10[t][j & 1]) : -INFINITY;
-        top = fmaxf(top, y[t][j]);
-      }
+      for (int j = 0; j < 4; j++) y[t][j] = fmaf(sc[t][j], sf[t][j & 1], -s.m10[t][j & 1]);
+    const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8
+    if (valid < kv::kTok)                           // the sequence's last granule
+#pragma unroll
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          if (t0 + j / 2 * 2 >= valid) y[t][j] = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; t++) top = fmaxf(fmaxf(fmaxf(y[t][0], y[t][1]), fmaxf(y[t][2], y[t][3])), top);
     if (__any_sync(kFull, top > kLogPMax)) {
+      const bool in0 = t0 < valid, in1 = t0 + 2 < valid;
 #pragma unroll
       for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -408,33 +451,24 @@ struct Kernel {
         ph[t][h] = transpose8x8(u);
       }
     }
-    // ---- value scales and biases of tokens 4c .. 4c+3; those behind the length are zero
-    const uint32_t k0 = (4 * c < valid ? 0xffffu : 0u) | (4 * c + 1 < valid ? 0xffff0000u : 0u);
-    const uint32_t k1 = (4 * c + 2 < valid ? 0xffffu : 0u) | (4 * c + 3 < valid ? 0xffff0000u : 0u);
-    const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG, *vb = vs + 32 * NG;
+    // ---- value scales and biases of tokens 4c .. 4c+3
+    const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG + c * 8, *vb = vs + 32 * NG;
     {
-      // the groups' powers of two: lane r checks group r % NG
+      // the groups' powers of two: lane r checks (and for r < NG holds the biases of) group r % NG
       const int g = r % NG;
-      uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32 + c * 8), b = *reinterpret_cast<const uint2 *>(vb + g * 32 + c * 8);
-      u.x &= k0; u.y &= k1; b.x &= k0; b.y &= k1;
-      const uint32_t su = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), bu = __vmaxu2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu);
-      // exponents that hold scale * 2^BITS and |bias| below 2^E
-      const int es = (int)max(su & 0xffffu, su >> 16) / 128 - 126 + BITS;
-      const int eb = (int)max(bu & 0xffffu, bu >> 16) / 128 - 126;
-      int need = max(es, eb);
-      need = min(need, 120);
-      int have = s.E[0];
-#pragma unroll
-      for (int i = 1; i < NG; i++) have = g == i ? s.E[i] : have;
-      if (__any_sync(kFull, need > have)) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32), b = *reinterpret_cast<const uint2 *>(vb + g * 32);
+      const uint32_t su = __vmaxu2(u.x, u.y) & 0x7fff7fffu, bu = __vmaxu2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu);
+      const uint32_t sm_ = max(su & 0xffffu, su >> 16), bm = max(bu & 0xffffu, bu >> 16);
+      if (__any_sync(kFull, (sm_ > s.lim_s) | (bm > s.lim_b))) {
+        // exponents that hold scale * 2^BITS and |bias| below 2^E
+        const int need = min(120, max((int)(sm_ >> 7) - 126 + BITS, (int)(bm >> 7) - 126));
 #pragma unroll
         for (int i = 0; i < NG; i++) {
-          int e = g == i ? need : -126;
-          e = __reduce_max_sync(kFull, e);
+          int e = __reduce_max_sync(kFull, g == i ? need : -126);
           if (e > s.E[i]) {
             e += 1;                                  // a little room, so that this stays rare
             const float f = p2(s.E[i] - e);
-            s.E[i] = e;
+            set_exponent(s, i, e, g == i);
 #pragma unroll
             for (int j = 0; j < VB; j++)
               if (j * DB / GS == i)
@@ -454,13 +488,10 @@ struct Kernel {
         }
       }
       // sum of P * (bias + Z scale): one MMA, row g of A = group g's biases
-      int e = s.E[0];
-#pragma unroll
-      for (int i = 1; i < NG; i++) e = g == i ? s.E[i] : e;
-      const float f = p2(-e), z = (float)(1 << (BITS - 1));
-      uint32_t a0 = pack_h2(fmaf(bf_lo(u.x), z, bf_lo(b.x)) * f, fmaf(bf_hi(u.x), z, bf_hi(b.x)) * f);
-      uint32_t a2 = pack_h2(fmaf(bf_lo(u.y), z, bf_lo(b.y)) * f, fmaf(bf_hi(u.y), z, bf_hi(b.y)) * f);
-      if (r >= NG) a0 = a2 = 0u;
+      const float z = (float)(1 << (BITS - 1)) * s.fb;
+      uint32_t a0 = pack_h2(fmaf(bf_lo(u.x), z, bf_lo(b.x) * s.fb), fmaf(bf_hi(u.x), z, bf_hi(b.x) * s.fb));
+      uint32_t a2 = pack_h2(fmaf(bf_lo(u.y), z, bf_lo(b.y) * s.fb), fmaf(bf_hi(u.y), z, bf_hi(b.y) * s.fb));
+      if (NG < 8 && r >= NG) a0 = a2 = 0u;
 #pragma unroll
       for (int t = 0; t < NT; t++) {
         mma(s.bacc[t], a0, 0u, a2, 0u, ph[t][0], ph[t][1]);
@@ -473,9 +504,8 @@ struct Kernel {
     const uint4 *vc = reinterpret_cast<const uint4 *>(sm + L.code_bytes) + lane;
 #pragma unroll
     for (int g = 0; g < NG; g++) {
-      uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32 + c * 8);
-      u.x &= k0; u.y &= k1;
-      const float f = p2(BITS - s.E[g]);
+      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32);
+      const float f = s.fs[g];
       const uint32_t s0 = pack_h2(bf_lo(u.x) * f, bf_hi(u.x) * f), s1 = pack_h2(bf_lo(u.y) * f, bf_hi(u.y) * f);
       uint32_t b[NT][2], bl[NT][2];
 #pragma unroll
@@ -563,9 +593,16 @@ struct Kernel {
   }
 };
 
-// Rounds and stores one output element.
-__device__ __forceinline__ void store_out(const Args &a, int64_t i, float v) {
-  a.out[i] = a.f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// Rounds and stores two output elements (i even).
+__device__ __forceinline__ void store_out2(const Args &a, int64_t i, float v0, float v1) {
+  uint32_t u;
+  if (a.f16) {
+    u = pack_h2(v0, v1);
+  } else {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
+    u = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  *reinterpret_cast<uint32_t *>(a.out + i) = u;
 }
 // log-sum-exp (natural) from the scaled max and total.
 __device__ __forceinline__ float lse_of(float m10, float l) {
@@ -602,32 +639,31 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
     }
   constexpr int kPart = Ws<D, K::GHP>::kPart;
   Rec *recs = reinterpret_cast<Rec *>(a.ws + (int64_t)2 * gridDim.x * kPart);
-  const long long mine = min(start.per, start.total - start.first);
-  if (mine <= 0 || start.b >= a.B) {
-    if (tid == 0) recs[blockIdx.x] = Rec{0, 0, 0, 0};
-    return;
-  }
-  // piece walked by the whole CTA (pc) and the copies of this warp (cp), ahead of it
+  // pieces walked by the whole CTA (pc), and this warp's copies (cp), ahead of it
   Cursor cp{}, pc{};
   cp.b = pc.b = start.b;
   cp.hc = pc.hc = start.hc;
-  cp.left = pc.left = mine;
-  cursor_open(a, pc, start.g, 0);
-  cursor_open(a, cp, start.g, warp);
-  cursor_settle(a, cp, warp);
-  if (tid == 0) recs[blockIdx.x] = Rec{start.b, start.hc, start.g, pc.n};
+  cp.left = pc.left = start.left;
+  if (!cursor_open<K::GB>(a, pc, start.u, 0)) {
+    if (tid == 0) recs[blockIdx.x] = Rec{0, 0, 0, 0};
+    return;
+  }
+  cursor_open<K::GB>(a, cp, start.u, warp);
+  cursor_settle<K::GB>(a, cp, warp);
+  if (tid == 0) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
 
   uint32_t filled = 0, phase = 0;     // slots with a copy, parity of each slot's next wait
   int slot_in = 0, slot_out = 0;
   bool dead = false;
+  const int64_t page_bytes = ((int64_t)a.H << a.gshift) * K::GB;
   auto issue = [&]() {                // the cursor's granule into slot_in
     if (cp.g >= cp.end) return;
     const int page = cp.page;
     if (page >= 0 && page < a.pages) {
       if (lane == 0) {
-        const int64_t off = (((int64_t)page * a.H + cp.hc / a.chunks) << a.gshift) + (cp.g & ((1 << a.gshift) - 1));
         mbar_arrive_expect_tx(bar + slot_in, K::GB);
-        bulk_load(ring + slot_in * K::GB, a.cache + off * K::GB, K::GB, bar + slot_in);
+        bulk_load(ring + slot_in * K::GB, cp.head + page * page_bytes + (cp.g & ((1 << a.gshift) - 1)) * K::GB, K::GB,
+                  bar + slot_in);
       }
       filled |= 1u << slot_in;
     } else if (lane == 0) {
@@ -636,12 +672,12 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
     slot_in = slot_in + 1 == a.depth ? 0 : slot_in + 1;
     cp.g += kWarps;
     cursor_page(a, cp);
-    cursor_settle(a, cp, warp);
+    cursor_settle<K::GB>(a, cp, warp);
   };
   for (int i = 0; i < a.depth; i++) issue();
 
   typename K::State s;
-  int g_first = start.g;
+  int g_first = pc.g;
   bool first_piece = true;
   while (true) {
     // ---- this piece's queries: chunk of heads [h0, h0 + heads) of kv head pc.hc / chunks
@@ -726,7 +762,10 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
     for (int g = g_first + warp; g < pc.end; g += kWarps) {
       if ((filled >> slot_out & 1u) && !dead) {
         if (mbar_wait(bar + slot_out, phase >> slot_out & 1u)) {
-          K::granule(ring + slot_out * K::GB, len - g * kv::kTok, qf, qsum, sf, s);
+          unsigned char *gran = ring + slot_out * K::GB;
+          const int valid = len - g * kv::kTok;
+          if (valid < kv::kTok) K::clear_tail(gran, valid);
+          K::granule(gran, valid, qf, qsum, sf, s);
           phase ^= 1u << slot_out;
           filled &= ~(1u << slot_out);
         } else {
@@ -767,10 +806,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
       if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t row = (int64_t)pc.b * a.H * a.G + h0 + h;
-        store_out(a, row * D + d, o.x * inv);
-        store_out(a, row * D + d + 1, o.y * inv);
-        store_out(a, row * D + d + 2, o.z * inv);
-        store_out(a, row * D + d + 3, o.w * inv);
+        store_out2(a, row * D + d, o.x * inv, o.y * inv);
+        store_out2(a, row * D + d + 2, o.z * inv, o.w * inv);
         if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
       } else {
         *reinterpret_cast<float4 *>(part + h * D + d) = o;
@@ -780,9 +817,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
         }
       }
     }
-    if (pc.left <= 0) break;
-    cursor_next_piece(a, pc, 0);
-    if (pc.end == 0) break;
+    if (!cursor_next_piece<K::GB>(a, pc, 0)) break;
     first_piece = false;
     g_first = 0;
     __syncthreads();
@@ -793,64 +828,88 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
       if (filled >> i & 1u) mbar_wait(bar + i, phase >> i & 1u);
 }
 
-// Joins the pieces of a (sequence, head chunk) that shares cut.  Block i looks at
-// the boundary in front of share i: if it is the first one inside its pair, the
-// block adds the piece that ends share i - 1 and those that begin share i, i + 1, ...
+// Joins the pieces of a pair that shares cut.  Blocks (i, h) look at the
+// boundary in front of share i: if it is the first one inside its pair, block h
+// adds head h of the piece that ends share i - 1 and of those that begin share
+// i, i + 1, ...: the warps take pieces in turn, a lane D / 32 elements.
 template <int D, int GHP>
 __global__ void __launch_bounds__(kThreads) k_attn_join(const Args a, int ctas) {
-  constexpr int kPart = Ws<D, GHP>::kPart;
+  constexpr int kPart = Ws<D, GHP>::kPart, E = D / 32;
+  __shared__ float so[kWarps][D], sml[kWarps][2];
   pdl_launch_dependents();
   pdl_wait();
   const Rec *recs = reinterpret_cast<const Rec *>(a.ws + (int64_t)2 * ctas * kPart);
-  const int i = blockIdx.x + 1;
+  const int i = blockIdx.x + 1, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (read through L2: nothing of the workspace may come from an earlier launch's lines in L1)
   auto rec_at = [&](int j) {
     const int4 v = __ldcg(reinterpret_cast<const int4 *>(recs + j));
     return Rec{v.x, v.y, v.z, v.w};
   };
-  const Rec rec = rec_at(i);
+  const Rec rec = rec_at(i), prev = rec_at(i - 1);
   if (rec.n == 0 || rec.g0 == 0) return;
-  const Rec prev = rec_at(i - 1);
   if (prev.b == rec.b && prev.hc == rec.hc && prev.g0 > 0) return;   // an earlier boundary is inside this pair
-  int last = i;                                                      // shares that begin inside the pair
-  while (last + 1 < ctas) {
-    const Rec nx = rec_at(last + 1);
-    if (nx.n == 0 || nx.b != rec.b || nx.hc != rec.hc || nx.g0 == 0) break;
-    last++;
-  }
   const int chunk = rec.hc % a.chunks;
   const int h0 = (rec.hc / a.chunks) * a.G + chunk * a.GH;
-  const int heads = min(a.GH, a.G - chunk * a.GH);
+  if (h >= min(a.GH, a.G - chunk * a.GH)) return;
+  int last = i;                                                      // shares that begin inside the pair
+  for (bool more = true; more;) {
+    const int j = last + 1 + lane;
+    Rec nx{0, 0, 0, 0};
+    if (j < ctas) nx = rec_at(j);
+    const unsigned in = __ballot_sync(kFull, nx.n != 0 && nx.b == rec.b && nx.hc == rec.hc && nx.g0 > 0);
+    const int got = in == kFull ? 32 : __ffs(~in) - 1;
+    last += got;
+    more = got == 32;
+  }
   // piece j = 0: end of share i - 1; j > 0: beginning of share i + j - 1
   auto part = [&](int j) { return a.ws + (int64_t)(j == 0 ? 2 * (i - 1) + 1 : 2 * (i + j - 1)) * kPart; };
   const int pieces = last - i + 2;
-  for (int e = threadIdx.x; e < heads * (D / 4); e += kThreads) {
-    const int h = e / (D / 4), d = e % (D / 4) * 4;
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-    for (int j = 0; j < pieces; j++) {
-      const float *p = part(j);
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + GHP * D + 2 * h));
-      const float mj = ml.x, lj = ml.y;
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + h * D + d));
-      if (lj == 0.0f) continue;
-      const float mn = fmaxf(m, mj);
-      const float fo = ex2(m - mn), fj = ex2(mj - mn);
-      m = mn;
-      l = fmaf(lj, fj, l * fo);
-      o.x = fmaf(v.x, fj, o.x * fo);
-      o.y = fmaf(v.y, fj, o.y * fo);
-      o.z = fmaf(v.z, fj, o.z * fo);
-      o.w = fmaf(v.w, fj, o.w * fo);
+  float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; e++) o[e] = 0.0f;
+#pragma unroll 4
+  for (int j = warp; j < pieces; j += kWarps) {
+    const float *p = part(j);
+    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + GHP * D + 2 * h));
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 t = __ldcg(reinterpret_cast<const float2 *>(p + h * D + lane * E + e));
+      v[e] = t.x;
+      v[e + 1] = t.y;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t row = (int64_t)rec.b * a.H * a.G + h0 + h;
-    store_out(a, row * D + d, o.x * inv);
-    store_out(a, row * D + d + 1, o.y * inv);
-    store_out(a, row * D + d + 2, o.z * inv);
-    store_out(a, row * D + d + 3, o.w * inv);
-    if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
+    const float mn = ml.y == 0.0f ? m : fmaxf(m, ml.x);              // (a piece without a token adds nothing)
+    const float fo = m == -INFINITY ? 0.0f : ex2(m - mn), fj = ml.y == 0.0f ? 0.0f : ex2(ml.x - mn);
+    m = mn;
+    l = fmaf(ml.y, fj, l * fo);
+#pragma unroll
+    for (int e = 0; e < E; e++) o[e] = ml.y == 0.0f ? o[e] : fmaf(v[e], fj, o[e] * fo);
   }
+#pragma unroll
+  for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    sml[warp][0] = m;
+    sml[warp][1] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x * 2 >= D) return;
+  float mt = -INFINITY, lt = 0.0f, x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++)
+    if (sml[w][1] != 0.0f) mt = fmaxf(mt, sml[w][0]);
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    if (sml[w][1] == 0.0f) continue;
+    const float f = ex2(sml[w][0] - mt);
+    lt = fmaf(sml[w][1], f, lt);
+    x0 = fmaf(so[w][2 * threadIdx.x], f, x0);
+    x1 = fmaf(so[w][2 * threadIdx.x + 1], f, x1);
+  }
+  const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+  const int64_t row = (int64_t)rec.b * a.H * a.G + h0 + h;
+  store_out2(a, row * D + 2 * threadIdx.x, x0 * inv, x1 * inv);
+  if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(mt, lt);
 }
 
 }  // namespace attn
@@ -876,7 +935,7 @@ attn::Args attn_args(const AttnCall &c) {
   while (gpp >>= 1) a.gshift++;
   const int64_t cap = c.max_pages * (c.cache.page_size / kv::kTok);
   a.cap_gran = (int)(cap < (1 << 27) ? cap : (1 << 27) - 1);   // (16 times this stays an int)
-  a.min_per = attn::kWarps;
+  a.min_per = attn::kPieceCost + attn::kWarps;
   a.f16 = c.f16;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   return a;
@@ -912,7 +971,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
-  cfg.gridDim = dim3((unsigned)(ctas - 1));
+  cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)a.GH);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, attn::k_attn_join<D, K::GHP>, a, ctas);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode join launch: %s", cudaGetErrorString(e));
