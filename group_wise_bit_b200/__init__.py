@@ -45,6 +45,7 @@ SIGNATURES = {
     "gwb_qpack_sym_i8": [_P, _I64, _I64, _P, _P, _P],
     "gwb_gemm_i8i8": [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P],
     "gwb_rmsnorm_quant_i8": [_P, _P, _P, _I64, _I64, _F64, _INT, _P, _P, _P, _P],
+    "gwb_dequant_per_token_i8": [_P, _P, _I64, _I64, _INT, _P, _P],
     "gwb_kv_block_bytes": [_I64, _INT, _INT, _INT, _P],
     "gwb_kv_write": [_P, _I64, _P, _I64, _P, _I64, _INT, _P, _I64, _I64, _I64, _INT, _INT, _INT, _P],
     "gwb_kv_read": [_P, _I64, _I64, _I64, _INT, _INT, _INT, _P, _I64, _INT, _P, _P, _P],
@@ -415,6 +416,19 @@ def rmsnorm_quant_i8(x, weight, eps, residual=None, residual_out=None, qx=None, 
     _call("gwb_rmsnorm_quant_i8", _ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _HALF[x.dtype],
           _ptr(residual_out), _ptr(qx), _ptr(sx), _stream())
     return qx, sx, residual_out
+
+
+def dequant_per_token_i8(qx, sx, dtype=torch.bfloat16, out=None):
+    """The values qx int8 [M, K] with scales sx fp32 [M] stand for, as bf16 or fp16 [M, K]."""
+    _dev(qx, "qx", (torch.int8,))
+    M, K = qx.shape
+    _dev(sx, "sx", (torch.float32,), (M,))
+    if dtype not in _HALF:
+        raise TypeError(f"dtype {dtype} not in {tuple(_HALF)}")
+    out = _out(out, "out", (M, K), dtype, qx.device)
+    _here(qx, sx, out)
+    _call("gwb_dequant_per_token_i8", _ptr(qx), _ptr(sx), M, K, _HALF[dtype], _ptr(out), _stream())
+    return out
 
 
 _block_bytes = {}

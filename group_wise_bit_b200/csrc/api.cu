@@ -494,10 +494,10 @@ gwb_status check_rows(const void *p, const char *name, int64_t stride, int64_t r
   return GWB_OK;
 }
 
-// The launch's blocks: 256 threads, 8 elements a thread, keys and values.
-gwb_status check_tokens(int64_t T, int64_t heads, int head_dim) {
+// (token, head) rows are numbered in 32 bits.
+gwb_status check_tokens(int64_t T, int64_t heads) {
   if (T < 0) return fail(GWB_ERR_INVALID_ARG, "negative T=%lld", (long long)T);
-  if (T >= kMaxDim || T * heads * 2 * (head_dim / 8) / 256 >= kMaxDim - 1)
+  if (T >= kMaxDim || T * heads >= kMaxDim)
     return fail(GWB_ERR_SHAPE, "T=%lld tokens of %lld heads exceed a launch", (long long)T, (long long)heads);
   return GWB_OK;
 }
@@ -528,6 +528,19 @@ gwb_status gwb_rmsnorm_quant_i8(const uint16_t *x, const uint16_t *residual, con
   return gwb::check_launch("rmsnorm_quant_i8");
 }
 
+gwb_status gwb_dequant_per_token_i8(const int8_t *qx, const float *sx, int64_t M, int64_t K, int dtype,
+                                    uint16_t *x_out, void *stream) {
+  if (M < 0 || K < 0) return fail(GWB_ERR_INVALID_ARG, "negative size (M=%lld, K=%lld)", (long long)M, (long long)K);
+  if (M >= kMaxDim || K >= kMaxDim) return fail(GWB_ERR_SHAPE, "M and K must be below 2^31");
+  GWB_TRY(check_dtype(dtype));
+  if (M == 0 || K == 0) return GWB_OK;
+  GWB_TRY(need(qx, "qx"));
+  GWB_TRY(need(sx, "sx"));
+  GWB_TRY(need(x_out, "x_out"));
+  gwb::launch_dequant_per_token_i8(qx, sx, M, K, dtype == GWB_F16, x_out, as_stream(stream));
+  return gwb::check_launch("dequant_per_token_i8");
+}
+
 gwb_status gwb_kv_block_bytes(int64_t page_size, int head_dim, int bits, int group_size, int64_t *bytes) {
   if (!bytes) return fail(GWB_ERR_INVALID_ARG, "bytes must not be NULL");
   GWB_TRY(check_cache(0, 1, page_size, head_dim, bits, group_size));
@@ -540,7 +553,7 @@ gwb_status gwb_kv_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, 
                         int64_t page_size, int head_dim, int bits, int group_size, void *stream) {
   GWB_TRY(check_cache(pages, heads, page_size, head_dim, bits, group_size));
   GWB_TRY(check_dtype(dtype));
-  GWB_TRY(check_tokens(T, heads, head_dim));
+  GWB_TRY(check_tokens(T, heads));
   if (T == 0) return GWB_OK;
   GWB_TRY(check_rows(k, "k", k_stride, heads * head_dim));
   GWB_TRY(check_rows(v, "v", v_stride, heads * head_dim));
@@ -556,7 +569,7 @@ gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t 
                        void *stream) {
   GWB_TRY(check_cache(pages, heads, page_size, head_dim, bits, group_size));
   GWB_TRY(check_dtype(dtype));
-  GWB_TRY(check_tokens(T, heads, head_dim));
+  GWB_TRY(check_tokens(T, heads));
   if (T == 0) return GWB_OK;
   GWB_TRY(need(k, "k"));
   GWB_TRY(need(v, "v"));

@@ -36,6 +36,8 @@ void launch_gptq_dequant(const int32_t *qweight, const uint16_t *scales, const i
                          int zadd = 1);
 void launch_quant_per_token_i8(const uint16_t *x, int64_t M, int64_t K, int8_t *qx, float *sx,
                                cudaStream_t st);
+void launch_dequant_per_token_i8(const int8_t *qx, const float *sx, int64_t M, int64_t K, bool f16, uint16_t *out,
+                                 cudaStream_t st);
 void launch_qpack_sym_i8(const float *w, int64_t N, int64_t K, int8_t *wq, float *sw, cudaStream_t st);
 void launch_qpack_sym_i4(const float *w, int64_t N, int64_t K, uint32_t *wq, float *sw, cudaStream_t st);
 

@@ -289,6 +289,40 @@ __global__ void __launch_bounds__(256) k_quant_per_token_i8(const uint16_t *__re
 }
 
 // ----------------------------------------------------------------------------
+// dequant_per_token_i8: 2^tshift threads a row (the block's other threads take
+// further rows), 16 codes a step where the width allows; one fp32 product a
+// value, rounded once.  Bound by the 3 bytes a value moves.
+template <bool F16, bool VEC>
+__global__ void __launch_bounds__(256) k_dequant_per_token_i8(const int8_t *__restrict__ qx,
+                                                              const float *__restrict__ sx, int64_t M, int64_t K,
+                                                              int tshift, uint16_t *__restrict__ out) {
+  const int64_t m = (int64_t)blockIdx.x * (256 >> tshift) + (threadIdx.x >> tshift);
+  if (m >= M) return;
+  const int t = threadIdx.x & ((1 << tshift) - 1);
+  const float s = sx[m];
+  auto value = [&](int q) {
+    const float f = __fmul_rn((float)q, s);
+    return F16 ? (uint32_t)__half_as_ushort(__float2half_rn(f)) : (uint32_t)bf16_bits(f);
+  };
+  const int8_t *row = qx + m * K;
+  uint16_t *dst = out + m * K;
+  if constexpr (VEC) {
+    for (int64_t i = t; i < K / 16; i += (int64_t)1 << tshift) {
+      const uint4 u = reinterpret_cast<const uint4 *>(row)[i];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        o[j] = value((int8_t)(w[j / 2] >> (j % 2 * 16))) | value((int8_t)(w[j / 2] >> (j % 2 * 16 + 8))) << 16;
+      reinterpret_cast<uint4 *>(dst)[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4 *>(dst)[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  } else {
+    for (int64_t i = t; i < K; i += (int64_t)1 << tshift) dst[i] = (uint16_t)value(row[i]);
+  }
+}
+
+// ----------------------------------------------------------------------------
 // qpack_sym_i4: one warp per output row; pass 1 reduces max|w|, pass 2 packs
 // eight two's-complement nibbles per word (lowest k in the lowest nibble).
 __global__ void __launch_bounds__(256) k_qpack_sym_i4(const float *__restrict__ w, int64_t N, int64_t K,
@@ -404,6 +438,19 @@ void launch_gptq_dequant(const int32_t *qweight, const uint16_t *scales, const i
 void launch_quant_per_token_i8(const uint16_t *x, int64_t M, int64_t K, int8_t *qx, float *sx,
                                cudaStream_t st) {
   k_quant_per_token_i8<<<(unsigned)M, 256, 0, st>>>(x, K, qx, sx);
+}
+
+void launch_dequant_per_token_i8(const int8_t *qx, const float *sx, int64_t M, int64_t K, bool f16, uint16_t *out,
+                                 cudaStream_t st) {
+  const bool vec = K % 16 == 0;
+  const int64_t steps = vec ? K / 16 : K;
+  int tshift = 3;
+  while (tshift < 8 && (1 << tshift) < steps) tshift++;
+  const unsigned grid = (unsigned)((M + (256 >> tshift) - 1) / (256 >> tshift));
+#define GWB_DQ(F, V) k_dequant_per_token_i8<F, V><<<grid, 256, 0, st>>>(qx, sx, M, K, tshift, out)
+  if (f16) vec ? GWB_DQ(true, true) : GWB_DQ(true, false);
+  else vec ? GWB_DQ(false, true) : GWB_DQ(false, false);
+#undef GWB_DQ
 }
 
 void launch_qpack_sym_i8(const float *w, int64_t N, int64_t K, int8_t *wq, float *sw, cudaStream_t st) {

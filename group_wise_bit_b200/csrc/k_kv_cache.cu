@@ -12,6 +12,7 @@
 #include "internal.h"
 #include "kv_layout.cuh"
 #include "ptx.cuh"
+#include "quotient.cuh"
 
 namespace gwb {
 namespace {
@@ -19,12 +20,6 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 
-// Monotone map of finite floats to int32 under the total order -0 < +0 (as qpack_affine).
-__device__ __forceinline__ int order_key(float f) {
-  const int i = __float_as_int(f);
-  return i >= 0 ? i : (i ^ 0x7fffffff);
-}
-__device__ __forceinline__ float key_to_float(int k) { return __int_as_float(k >= 0 ? k : (k ^ 0x7fffffff)); }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
@@ -51,27 +46,24 @@ struct KvArgs {
   int64_t k_stride, v_stride;
   const int64_t *slots;
   unsigned char *cache;
-  int64_t T, total_slots;
-  int H, page_size;
+  int64_t total_slots;
+  uint32_t rows;               // T * H
+  int H, page_shift;
 };
 
-// This lane's place: row (token, head, key / value) and element 8 * l in it.
+// This lane's place: row (token, head) and element 8 * l in it; blockIdx.y: keys or values.
 struct Place {
-  int64_t t;
-  int h, what, l;
-  bool in;
+  uint32_t row, t;
+  int h, l;
 };
 template <int D>
 __device__ __forceinline__ Place place_of(const KvArgs &a) {
   constexpr int LR = D / 8;
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / LR;
   Place p;
+  p.row = blockIdx.x * (kThreads / LR) + threadIdx.x / LR;
   p.l = threadIdx.x % LR;
-  p.what = (int)(i & 1);
-  const int64_t th = i >> 1;
-  p.t = th / a.H;
-  p.h = (int)(th - p.t * a.H);
-  p.in = p.t < a.T;
+  p.t = p.row / (uint32_t)a.H;
+  p.h = (int)(p.row - p.t * (uint32_t)a.H);
   return p;
 }
 
@@ -83,9 +75,9 @@ __device__ __forceinline__ bool granule_of(const KvArgs &a, int64_t slot, int h,
     atomicOr(&g_device_error, kErrIndex);
     return false;
   }
-  const int64_t page = slot / a.page_size;
-  const int in_page = (int)(slot - page * a.page_size);
-  *off = ((page * a.H + h) * (a.page_size / kv::kTok) + in_page / kv::kTok) * (int64_t)granule;
+  const int64_t page = slot >> a.page_shift;
+  const int in_page = (int)slot & ((1 << a.page_shift) - 1);
+  *off = (((page * a.H + h) << a.page_shift) + in_page) / kv::kTok * granule;
   *tok = in_page % kv::kTok;
   return true;
 }
@@ -96,40 +88,68 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const KvArgs a) {
   constexpr int LG = GS / 8;              // lanes of a group
   constexpr float QMAX = (float)((1 << BITS) - 1);
   const Place p = place_of<D>(a);
+  const bool val = blockIdx.y != 0;
   int64_t off = 0;
   int tok = 0;
-  const bool live = p.in && granule_of(a, __ldg(a.slots + p.t), p.h, L.granule, &off, &tok);
+  const bool live = p.row < a.rows && granule_of(a, __ldg(a.slots + p.t), p.h, L.granule, &off, &tok);
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (live) {
-    const uint16_t *row = p.what ? a.v + p.t * a.v_stride : a.k + p.t * a.k_stride;
-    unpack8<F16>(*reinterpret_cast<const uint4 *>(row + p.h * D + p.l * 8), v);
+    const uint16_t *row = val ? a.v + p.t * a.v_stride : a.k + p.t * a.k_stride;
+    unpack8<F16>(__ldg(reinterpret_cast<const uint4 *>(row + p.h * D + p.l * 8)), v);
   }
-  int kmin = order_key(v[0]), kmax = kmin;
+  // (min and max order -0 below +0, as qpack_affine's keys do)
+  float mn = v[0], mx = v[0];
 #pragma unroll
   for (int j = 1; j < 8; j++) {
-    kmin = min(kmin, order_key(v[j]));
-    kmax = max(kmax, order_key(v[j]));
+    mn = fminf(mn, v[j]);
+    mx = fmaxf(mx, v[j]);
   }
 #pragma unroll
   for (int o = 1; o < LG; o <<= 1) {
-    kmin = min(kmin, __shfl_xor_sync(kFull, kmin, o));
-    kmax = max(kmax, __shfl_xor_sync(kFull, kmax, o));
+    mn = fminf(mn, __shfl_xor_sync(kFull, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
   }
   if (!live) return;
-  const float mn = key_to_float(kmin), mx = key_to_float(kmax);
   const float s = __fdiv_rn(__fsub_rn(mx, mn), QMAX);
-  uint32_t words[BITS / 4] = {};
+  const Divisor d = make_divisor(s);
+  uint32_t words[BITS / 4];
+  if (d.fast) {
+    // integers n in the low bits of the rounded quotients; no code passes QMAX (quotients are within 2^-23 of it)
+    float z[8];
 #pragma unroll
-  for (int j = 0; j < 8; j++) {
-    uint32_t q = 0;
-    if (s != 0.0f) q = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[j], mn), s)), 0.0f), QMAX);
-    words[j * BITS / 32] |= q << (j * BITS % 32);
+    for (int j = 0; j < 8; j++) z[j] = round_bits(quotient_fast(__fsub_rn(v[j], mn), d));
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+        words[i] = __byte_perm(__byte_perm(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]), 0x0040),
+                               __byte_perm(__float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3]), 0x0040), 0x5410);
+    } else {
+      // four nibbles at a time in fp32: exact below 2^16
+      uint32_t h[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        float n[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) n[j] = __fsub_rn(z[4 * i + j], kRoundMagic);
+        h[i] = __float_as_uint(round_bits(fmaf(fmaf(n[3], 16.0f, n[2]), 256.0f, fmaf(n[1], 16.0f, n[0]))));
+      }
+      words[0] = __byte_perm(h[0], h[1], 0x5410);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < BITS / 4; i++) words[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      uint32_t q = 0;
+      if (s != 0.0f) q = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[j], mn), s)), 0.0f), QMAX);
+      words[j * BITS / 32] |= q << (j * BITS % 32);
+    }
   }
   unsigned char *gran = a.cache + off;
 #pragma unroll
   for (int i = 0; i < BITS / 4; i++) {
     const int w = p.l * (BITS / 4) + i;
-    if (p.what == 0) {
+    if (!val) {
       *reinterpret_cast<uint32_t *>(gran + kv::key_word(L, tok, w)) = words[i];
     } else {
       *reinterpret_cast<uint16_t *>(gran + kv::val_half(L, tok, 2 * w)) = (uint16_t)words[i];
@@ -138,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const KvArgs a) {
   }
   if (p.l % LG == 0) {
     const int g = p.l / LG;
-    if (p.what == 0) {
+    if (!val) {
       *reinterpret_cast<uint32_t *>(gran + kv::key_meta(L, tok, g)) = bf16_bits(s) | (bf16_bits(mn) << 16);
     } else {
       *reinterpret_cast<uint16_t *>(gran + kv::val_scale(L, tok, g)) = (uint16_t)bf16_bits(s);
@@ -151,48 +171,59 @@ template <int BITS, int D, int GS, bool F16>
 __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a) {
   constexpr kv::Layout L = kv::layout(BITS, D, GS);
   const Place p = place_of<D>(a);
-  if (!p.in) return;
+  if (p.row >= a.rows) return;
+  const bool val = blockIdx.y != 0;
   int64_t off = 0;
   int tok = 0;
   uint32_t o[4] = {0, 0, 0, 0};
   if (granule_of(a, __ldg(a.slots + p.t), p.h, L.granule, &off, &tok)) {
     const unsigned char *gran = a.cache + off;
     uint32_t words[BITS / 4];
-#pragma unroll
-    for (int i = 0; i < BITS / 4; i++) {
-      const int w = p.l * (BITS / 4) + i;
-      if (p.what == 0)
-        words[i] = *reinterpret_cast<const uint32_t *>(gran + kv::key_word(L, tok, w));
-      else
-        words[i] = (uint32_t)*reinterpret_cast<const uint16_t *>(gran + kv::val_half(L, tok, 2 * w)) |
-                   (uint32_t)*reinterpret_cast<const uint16_t *>(gran + kv::val_half(L, tok, 2 * w + 1)) << 16;
-    }
     const int g = p.l / (GS / 8);
     float s, b;
-    if (p.what == 0) {
+    if (!val) {
+#pragma unroll
+      for (int i = 0; i < BITS / 4; i++)
+        words[i] = *reinterpret_cast<const uint32_t *>(gran + kv::key_word(L, tok, p.l * (BITS / 4) + i));
       const uint32_t m = *reinterpret_cast<const uint32_t *>(gran + kv::key_meta(L, tok, g));
       s = bf16_lo(m);
       b = bf16_hi(m);
     } else {
+#pragma unroll
+      for (int i = 0; i < BITS / 4; i++) {
+        const int w = p.l * (BITS / 4) + i;
+        words[i] = (uint32_t)*reinterpret_cast<const uint16_t *>(gran + kv::val_half(L, tok, 2 * w)) |
+                   (uint32_t)*reinterpret_cast<const uint16_t *>(gran + kv::val_half(L, tok, 2 * w + 1)) << 16;
+      }
       s = bf16_lo(*reinterpret_cast<const uint16_t *>(gran + kv::val_scale(L, tok, g)));
       b = bf16_lo(*reinterpret_cast<const uint16_t *>(gran + kv::val_bias(L, tok, g)));
     }
+    float f[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const uint32_t q = (words[j * BITS / 32] >> (j * BITS % 32)) & ((1u << BITS) - 1u);
-      const float f = __fmaf_rn((float)q, s, b);   // fp32(code * scale + bias), then the output's rounding
-      const uint32_t h = F16 ? (uint32_t)__half_as_ushort(__float2half_rn(f)) : bf16_bits(f);
-      o[j / 2] |= h << (j % 2 * 16);
+      // a code in the low bits of 2^23's significand, made a number by a subtraction (exact)
+      const uint32_t q = ((words[j * BITS / 32] >> (j * BITS % 32)) & ((1u << BITS) - 1u)) | 0x4b000000u;
+      f[j] = __fmaf_rn(__fsub_rn(__uint_as_float(q), 8388608.0f), s, b);   // fp32(code * scale + bias)
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t *>(&h);
+      }
     }
   }
-  uint16_t *dst = (p.what ? a.vo : a.ko) + (p.t * a.H + p.h) * D + p.l * 8;
+  uint16_t *dst = (val ? a.vo : a.ko) + (int64_t)p.row * D + p.l * 8;
   *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int BITS, int D, int GS>
 void launch(const KvArgs &a, bool f16, bool write, cudaStream_t st) {
-  const int64_t rows = a.T * a.H * 2;
-  const unsigned grid = (unsigned)((rows * (D / 8) + kThreads - 1) / kThreads);
+  constexpr uint32_t per = kThreads / (D / 8);          // rows of a block
+  const dim3 grid((a.rows + per - 1) / per, 2);
   if (write) {
     if (f16) k_kv_write<BITS, D, GS, true><<<grid, kThreads, 0, st>>>(a);
     else k_kv_write<BITS, D, GS, false><<<grid, kThreads, 0, st>>>(a);
@@ -222,10 +253,11 @@ void launch_kv_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int
                      int64_t T, const KvCache &c, bool f16, cudaStream_t st) {
   KvArgs a{};
   a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride;
-  a.slots = slots; a.T = T;
+  a.slots = slots; a.rows = (uint32_t)(T * c.heads);
   a.cache = static_cast<unsigned char *>(c.data);
   a.total_slots = c.pages * c.page_size;
-  a.H = (int)c.heads; a.page_size = (int)c.page_size;
+  a.H = (int)c.heads;
+  while ((1 << a.page_shift) < c.page_size) a.page_shift++;
   dispatch(a, c.head_dim, c.bits, c.gs, f16, true, st);
 }
 
@@ -233,10 +265,11 @@ void launch_kv_read(const KvCache &c, const int64_t *slots, int64_t T, uint16_t 
                     cudaStream_t st) {
   KvArgs a{};
   a.ko = k; a.vo = v;
-  a.slots = slots; a.T = T;
+  a.slots = slots; a.rows = (uint32_t)(T * c.heads);
   a.cache = static_cast<unsigned char *>(c.data);
   a.total_slots = c.pages * c.page_size;
-  a.H = (int)c.heads; a.page_size = (int)c.page_size;
+  a.H = (int)c.heads;
+  while ((1 << a.page_shift) < c.page_size) a.page_shift++;
   dispatch(a, c.head_dim, c.bits, c.gs, f16, false, st);
 }
 

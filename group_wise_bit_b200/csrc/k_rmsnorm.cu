@@ -16,12 +16,13 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "quotient.cuh"
 
 namespace gwb {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMaxThreads = 1024;
+constexpr int64_t kManyRows = 592;   // four rows an SM
 
 template <bool F16>
 __device__ __forceinline__ float to_f(uint16_t h) {
@@ -34,15 +35,26 @@ __device__ __forceinline__ uint16_t from_f(float f) {
   else return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
-// rint(y / s) clipped to +-127, the division correctly rounded.  `inv` is about
-// 1 / s: y * inv is within 127 * 2^-22 of the quotient, so away from a rounding
-// border (by far more than that) both round to the same integer, and only
-// quotients within 2^-12 of one take the division.
-__device__ __forceinline__ int quant(float y, float s, float inv) {
-  float t = __fmul_rn(y, inv);
-  float n = rintf(t);
-  if (fabsf(fabsf(__fsub_rn(t, n)) - 0.5f) < 0x1p-12f) n = rintf(__fdiv_rn(y, s));
-  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
+// The int8 code of y over a row's scale, by the division itself.
+__device__ __forceinline__ int quant_slow(float y, float s) {
+  return s == 0.0f ? 0 : (int)fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f);
+}
+
+// Two values of 16 bits a word, as fp32.
+template <bool F16>
+__device__ __forceinline__ float2 to_f2(uint32_t w) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t from_f2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -89,93 +101,98 @@ __device__ __forceinline__ float block_max(float v, float *red) {
 // One row a block, the row in registers: V runs of 8 elements a thread, 16-byte
 // loads where the width is a multiple of 8 (VEC), single elements otherwise.
 template <int V, bool VEC, bool F16>
-__global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_row(const NormArgs a) {
+__global__ void __launch_bounds__(V > 2 ? 512 : 1024) k_rmsnorm_row(const NormArgs a) {
   __shared__ double red_d[32];
   __shared__ float red_f[32], rstd_s;
-  const int64_t m = blockIdx.x, K = a.K;
-  const int nt = blockDim.x, tid = threadIdx.x;
-  const uint16_t *x = a.x + m * K;
-  const uint16_t *res = a.residual ? a.residual + m * K : nullptr;
-  auto at = [&](int v, int e) { return VEC ? ((int64_t)v * nt + tid) * 8 + e : (int64_t)(v * 8 + e) * nt + tid; };
+  const int64_t m = blockIdx.x;
+  const int K = (int)a.K, nt = blockDim.x, tid = threadIdx.x;
+  const uint16_t *x = a.x + m * K, *res = a.residual ? a.residual + m * K : nullptr;
+  // element e of run v: a run is contiguous (VEC) or a column of the block's stride
+  auto at = [&](int v, int e) { return VEC ? (v * nt + tid) * 8 + e : (v * 8 + e) * nt + tid; };
+  auto load = [&](const uint16_t *p, int v) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if constexpr (VEC) {
+      if (at(v, 0) < K) u = *reinterpret_cast<const uint4 *>(p + at(v, 0));
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        if (at(v, e) < K) w[e / 2] |= (uint32_t)p[at(v, e)] << (e % 2 * 16);
+      u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return u;
+  };
 
-  float h[V][8];
+  uint4 xr[V], rr[V];
+#pragma unroll
+  for (int v = 0; v < V; v++) {
+    xr[v] = load(x, v);
+    if (res) rr[v] = load(res, v);
+  }
   double sum = 0.0;
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    uint16_t raw[8], rr[8];
-    if constexpr (VEC) {
-      uint4 u = make_uint4(0, 0, 0, 0), w = make_uint4(0, 0, 0, 0);
-      if (at(v, 0) < K) {
-        u = *reinterpret_cast<const uint4 *>(x + at(v, 0));
-        if (res) w = *reinterpret_cast<const uint4 *>(res + at(v, 0));
-      }
-      *reinterpret_cast<uint4 *>(raw) = u;
-      *reinterpret_cast<uint4 *>(rr) = w;
-    } else {
+    uint32_t w[4] = {xr[v].x, xr[v].y, xr[v].z, xr[v].w};
+    if (res) {
+      const uint32_t r4[4] = {rr[v].x, rr[v].y, rr[v].z, rr[v].w};
 #pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const bool in = at(v, e) < K;
-        raw[e] = in ? x[at(v, e)] : 0;
-        rr[e] = in && res ? res[at(v, e)] : 0;
+      for (int i = 0; i < 4; i++) {
+        const float2 f = to_f2<F16>(w[i]), g = to_f2<F16>(r4[i]);
+        w[i] = from_f2<F16>(__fadd_rn(f.x, g.x), __fadd_rn(f.y, g.y));
       }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      float f = to_f<F16>(raw[e]);
-      if (res) {
-        raw[e] = from_f<F16>(__fadd_rn(f, to_f<F16>(rr[e])));
-        f = to_f<F16>(raw[e]);
-      }
-      h[v][e] = f;
-      sum = fma((double)f, (double)f, sum);
-    }
-    if (a.residual_out) {
       uint16_t *dst = a.residual_out + m * K;
       if constexpr (VEC) {
-        if (at(v, 0) < K) *reinterpret_cast<uint4 *>(dst + at(v, 0)) = *reinterpret_cast<const uint4 *>(raw);
+        if (at(v, 0) < K) *reinterpret_cast<uint4 *>(dst + at(v, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; e++)
-          if (at(v, e) < K) dst[at(v, e)] = raw[e];
+          if (at(v, e) < K) dst[at(v, e)] = (uint16_t)(w[e / 2] >> (e % 2 * 16));
       }
     }
+    xr[v] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float2 f = to_f2<F16>(w[i]);
+      sum = fma((double)f.x, (double)f.x, sum);
+      sum = fma((double)f.y, (double)f.y, sum);
+    }
   }
-  const float r = block_rstd(sum, red_d, &rstd_s, K, a.eps);
+  const float r = block_rstd(sum, red_d, &rstd_s, a.K, a.eps);
 
-  float amax = 0.0f;
+  float y[V][8], amax = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    uint16_t w[8];
-    if constexpr (VEC) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (at(v, 0) < K) u = __ldg(reinterpret_cast<const uint4 *>(a.weight + at(v, 0)));
-      *reinterpret_cast<uint4 *>(w) = u;
-    } else {
+    const uint4 wv = load(a.weight, v);
+    const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w}, h[4] = {xr[v].x, xr[v].y, xr[v].z, xr[v].w};
 #pragma unroll
-      for (int e = 0; e < 8; e++) w[e] = at(v, e) < K ? __ldg(a.weight + at(v, e)) : (uint16_t)0;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      h[v][e] = __fmul_rn(__fmul_rn(h[v][e], r), to_f<F16>(w[e]));
-      amax = fmaxf(amax, fabsf(h[v][e]));
+    for (int i = 0; i < 4; i++) {
+      const float2 f = to_f2<F16>(h[i]), g = to_f2<F16>(w[i]);
+      y[v][2 * i] = __fmul_rn(__fmul_rn(f.x, r), g.x);
+      y[v][2 * i + 1] = __fmul_rn(__fmul_rn(f.y, r), g.y);
+      amax = fmaxf(fmaxf(fabsf(y[v][2 * i]), fabsf(y[v][2 * i + 1])), amax);
     }
   }
   amax = block_max(amax, red_f);
   const float s = __fdiv_rn(amax, 127.0f);
-  const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-  const bool ok = inv <= 3.0e38f;                     // s so small that 1 / s overflows: divide
+  const Divisor d = make_divisor(s);
   if (tid == 0) a.sx[m] = s;
   int8_t *q = a.qx + m * K;
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    int c[8];
+    // |y| <= 127 s (1 + 2^-23), so no code passes 127; the low byte of the rounded quotient is the code
+    uint32_t c[8];
+    if (d.fast) {
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-      c[e] = s == 0.0f ? 0 : ok ? quant(h[v][e], s, inv) : (int)fminf(fmaxf(rintf(__fdiv_rn(h[v][e], s)), -127.0f), 127.0f);
+      for (int e = 0; e < 8; e++) c[e] = __float_as_uint(round_bits(quotient_fast(y[v][e], d)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++) c[e] = (uint32_t)quant_slow(y[v][e], s);
+    }
     if constexpr (VEC) {
-      uint32_t o[2] = {0, 0};
+      uint32_t o[2];
 #pragma unroll
-      for (int e = 0; e < 8; e++) o[e / 4] |= ((uint32_t)c[e] & 0xffu) << (e % 4 * 8);
+      for (int i = 0; i < 2; i++)
+        o[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
       if (at(v, 0) < K) *reinterpret_cast<uint2 *>(q + at(v, 0)) = make_uint2(o[0], o[1]);
     } else {
 #pragma unroll
@@ -188,7 +205,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_row(const NormArgs a) {
 // Rows too wide for the registers of one block (K > 32768): the same steps with
 // the row read again for each (from L2 for all but the first).
 template <bool F16>
-__global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_wide(const NormArgs a) {
+__global__ void __launch_bounds__(1024) k_rmsnorm_wide(const NormArgs a) {
   __shared__ double red_d[32];
   __shared__ float red_f[32], rstd_s;
   const int64_t m = blockIdx.x, K = a.K;
@@ -216,7 +233,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_wide(const NormArgs a) 
   if (threadIdx.x == 0) a.sx[m] = s;
   for (int64_t i = threadIdx.x; i < K; i += blockDim.x) {
     const float y = __fmul_rn(__fmul_rn(value(i, false), r), to_f<F16>(__ldg(a.weight + i)));
-    a.qx[m * K + i] = s == 0.0f ? (int8_t)0 : (int8_t)fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f);
+    a.qx[m * K + i] = (int8_t)quant_slow(y, s);
   }
 }
 
@@ -226,12 +243,16 @@ void launch(const NormArgs &a, int64_t M, cudaStream_t st) {
   const bool vec = a.K % 8 == 0;
   const unsigned grid = (unsigned)M;
   auto threads = [&](int V) { return (unsigned)((runs + (int64_t)V * 32 - 1) / ((int64_t)V * 32) * 32); };
+  // Few rows: as many threads a row as its runs allow, for the latency of one row.
+  // Many rows: up to four runs a thread, for the two reductions' cost a row.
+  const int64_t want = M >= kManyRows ? (runs >= 256 ? 4 : (runs >= 64 ? 2 : 1)) : 1;
 #define GWB_NORM(V, VEC) k_rmsnorm_row<V, VEC, F16><<<grid, threads(V), 0, st>>>(a)
-  if (runs <= kMaxThreads) return vec ? GWB_NORM(1, true) : GWB_NORM(1, false);
-  if (runs <= 2 * kMaxThreads) return vec ? GWB_NORM(2, true) : GWB_NORM(2, false);
-  if (runs <= 4 * kMaxThreads) return vec ? GWB_NORM(4, true) : GWB_NORM(4, false);
+  if (runs <= 1024 && want == 1) return vec ? GWB_NORM(1, true) : GWB_NORM(1, false);
+  if (runs <= 2048 && want <= 2) return vec ? GWB_NORM(2, true) : GWB_NORM(2, false);
+  if (runs <= 2048) return vec ? GWB_NORM(4, true) : GWB_NORM(4, false);
+  if (runs <= 4096) return vec ? GWB_NORM(8, true) : GWB_NORM(8, false);
 #undef GWB_NORM
-  k_rmsnorm_wide<F16><<<grid, kMaxThreads, 0, st>>>(a);
+  k_rmsnorm_wide<F16><<<grid, 1024, 0, st>>>(a);
 }
 
 }  // namespace

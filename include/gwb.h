@@ -356,6 +356,13 @@ gwb_status gwb_rmsnorm_quant_i8(const uint16_t *x, const uint16_t *residual, con
                                 int64_t M, int64_t K, double eps, int dtype, uint16_t *residual_out,
                                 int8_t *qx, float *sx, void *stream);
 
+/* dequant_per_token_i8 -- x_out[m,k] = round(fp32(qx[m,k] * sx[m])), the values
+ * that gwb_quant_per_token_i8's or gwb_rmsnorm_quant_i8's output stands for, for
+ * products that take 16-bit activations.
+ *   qx int8 [M, K], sx fp32 [M], x_out bf16 / fp16 (`dtype`) [M, K].  Bit-exact. */
+gwb_status gwb_dequant_per_token_i8(const int8_t *qx, const float *sx, int64_t M, int64_t K, int dtype,
+                                    uint16_t *x_out, void *stream);
+
 /* ------------------------------------------------------------------ quantized paged cache
  * Keys and values of past tokens, quantized group-wise in the MLX affine scheme
  * (gwb_qpack_affine's arithmetic along the head dimension) and kept in pages.

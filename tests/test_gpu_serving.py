@@ -102,6 +102,16 @@ def test_norm_equals_the_quantizer_where_the_norm_is_exact():
     assert torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 16), (5, 17), (2, 4096), (300, 144), (7, 5003)])
+def test_dequant_per_token_bit_exact(M, K, dt):
+    rng = np.random.default_rng(K)
+    q = rng.integers(-128, 128, (M, K)).astype(np.int8)
+    s = (np.exp(3 * rng.standard_normal(M)) * (rng.random(M) > 0.2)).astype(np.float32)
+    got = gwb.dequant_per_token_i8(torch.tensor(q).to(DEV), torch.tensor(s).to(DEV), dtype=DT[dt])
+    assert np.array_equal(_np(got), S.rnd(q.astype(np.float32) * s[:, None], dt == "fp16"))
+
+
 # ------------------------------------------------------------------ cache
 LAYOUTS = [(b, D, g) for b in (4, 8) for D in (64, 128, 256) for g in (32, 64, 128) if g <= D]
 
@@ -119,6 +129,7 @@ def test_cache_write_and_read_bit_exact(bits, D, gs, dt):
     T = 37
     k, v = _rand(rng, (T, H, D), dt), _rand(rng, (T, H, D), dt, 5.0)
     k[0, 0] = 0.0
+    k[0, 0, 5] = -0.0                                 # a group of both zeros: its bias is -0
     k[1, 1, 3] = -0.0
     v[2, 2] = 1.25                                    # constant groups
     v[3, 0, ::7] *= 100
@@ -152,6 +163,28 @@ def test_cache_rows_are_the_affine_packers():
     wq, sc, bi = gwb.qpack_affine(k.float().reshape(100, 128).contiguous(), 4, 64)
     ref = gwb.dequant_affine(wq, sc, bi, 128, 4, 64).view(50, 2, 128)
     assert torch.equal(kr, ref) and torch.equal(vr, ref)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_cache_codes_on_the_border(bits):
+    """Rows of few distinct bf16 values put many quotients halfway between two codes, and scales over all
+    exponents and significands: the same codes as the packer, which divides."""
+    g = torch.Generator(device=DEV).manual_seed(bits)
+    T, D, gs = 6000, 128, 32
+    k = torch.randint(-24, 25, (T, 1, D), device=DEV, generator=g).float()
+    step = torch.exp2(torch.randint(-60, 60, (T, 1, 1), device=DEV, generator=g).float())
+    step *= 1 + torch.randint(0, 128, (T, 1, 1), device=DEV, generator=g) / 128
+    k = (k * step).bfloat16()
+    v = torch.randn(T, 1, D, device=DEV, generator=g).mul_(step).bfloat16()
+    cache = gwb.kv_cache(-(-T // 16), 1, D, 16, bits, gs)
+    gwb.kv_write(cache, torch.arange(T, device=DEV), k, v, bits, gs)
+    for x, what in ((k, "k"), (v, "v")):
+        wq, sc, bi = gwb.qpack_affine(x.float().reshape(T, D).contiguous(), bits, gs)
+        code, s, b = S.parts_of(cache.cpu().numpy(), np.arange(T), what, bits, D, gs, 16)
+        words = wq.cpu().numpy().view(np.uint32)
+        ref = (words[:, :, None] >> (np.arange(32 // bits, dtype=np.uint32) * bits)) & ((1 << bits) - 1)
+        assert np.array_equal(code.reshape(T, D), ref.reshape(T, D))
+        assert np.array_equal(s.reshape(T, -1), _np(sc)) and np.array_equal(b.reshape(T, -1), _np(bi))
 
 
 @pytest.mark.parametrize("T", [1, 2, 300])

@@ -47,6 +47,14 @@ def test_norm_refusals():
     assert call(M=0, x=NULL, w=NULL, qx=NULL, sx=NULL) == 0
 
 
+def test_dequant_per_token_refusals():
+    def call(q=OK16, s=OK16, M=2, K=64, dt=0, out=OK16):
+        return _st("gwb_dequant_per_token_i8", q, s, M, K, dt, out, NULL)
+    assert call(M=-1) == 1 and call(K=1 << 31) == 2 and call(dt=5) == 3
+    assert call(q=NULL) == 1 and call(s=BAD) == 4 and call(out=OK8) == 4
+    assert call(M=0, q=NULL, s=NULL, out=NULL) == 0
+
+
 def _cache_args(**kw):
     d = dict(pages=4, heads=2, page=16, D=64, bits=4, gs=32)
     d.update(kw)
@@ -88,8 +96,8 @@ def test_write_and_read_refusals():
     assert read(k=NULL) == 1 and read(v=NULL) == 1 and read(slots=NULL) == 1 and read(cache=NULL) == 1
     assert read(k=OK8) == 4 and read(v=OK8) == 4 and read(cache=BAD) == 4
     assert read(T=0, k=NULL, v=NULL, slots=NULL, cache=NULL) == 0
-    # more rows than one launch's blocks can name
-    assert _st("gwb_kv_read", OK16, 4, 65535, 16, 256, 4, 32, OK16, 1 << 20, 0, OK16, OK16, NULL) == 2
+    # more (token, head) rows than 32 bits number
+    assert _st("gwb_kv_read", OK16, 4, 65535, 16, 256, 4, 32, OK16, 1 << 16, 0, OK16, OK16, NULL) == 2
 
 
 def test_attention_refusals():
