@@ -9,22 +9,26 @@
 // so neither keys nor values are ever dequantized: the codes are the MMA's
 // operand and the group scales multiply 16-token score fragments and P.
 //
-// Work split.  The unit is a granule (16 tokens of one head, one contiguous
-// bulk copy).  The granules of all (sequence, head) pairs form one line, cut
+// Work split.  The unit is two granules (32 tokens of one head, one contiguous
+// bulk copy where a page holds both).  The units of all (sequence, head) pairs form one line, cut
 // into equal shares, one a CTA; every CTA finds its share from the lengths on
 // the device, so ragged batches and lengths that change between graph replays
 // are balanced and the host never reads a length.  A (sequence, head) that is
 // cut leaves one partial (fp32 sums, max, total) a piece, joined by a second,
 // dependent launch in a fixed order (no atomics: results are reproducible).
-// In a CTA the warps take granules in turn, each streaming its own through a
+// In a CTA the warps take units in turn, each streaming its own through a
 // private ring of bulk copies, and join through shared memory.
 //
 // Codes enter the m16n8k16 fp16 MMA as subnormals: code bits in the low bits of
 // an fp16 are code * 2^-24, exactly, so unpacking is one AND per register (two
 // codes), with a shift for every other pair; the nibble at bits 4..7 stands for
-// 16 * code and its q is divided by 16 (exact) or its sum at the end.  Value
-// codes are centred with an exact HADD2, because the sum of uncentred codes is
-// far larger than the result and the tensor core truncates its accumulator.
+// 16 * code and its q is divided by 16 (exact) or its sum at the end.  The sum of
+// uncentred value codes is far larger than the result and the tensor core
+// truncates what it adds (toward zero; a subnormal operand at its type's smallest
+// normal exponent, 2^-14 of a code here), so every granule's sum is centred at once
+// by an MMA with a constant operand of -Z: one issue slot where subtracting Z from
+// the unpacked registers takes four.  With PREC the codes do go through 1024 + code
+// and a subtraction instead, which makes them normal numbers and the products exact.
 //
 // Precision.  q is scaled by a power of two per head into fp16 (exact for bf16
 // and fp16 but for elements 2^-27 below the largest).  Scores, maxima, totals
@@ -64,16 +68,16 @@ struct Args {
   int64_t pages;
   int B, H, G, GH;              // GH: query heads of one chunk
   int chunks;                   // chunks of a kv head's G query heads
-  int gshift, cap_gran;         // log2 of a page's granules; granules a table row can name
+  int gshift, cap;              // log2 of a page's granules; tokens a table row can name
   int depth;                    // ring slots a warp
-  int min_per;                  // least granules of a share
+  int min_per;                  // least places of a share
   int f16;
   float scale_log2;             // softmax scale * log2 e
 };
 
 // One record a CTA: the first piece of its share.
 struct Rec {
-  int b, hc, g0, n;             // sequence, head chunk, first granule, granules of the sequence (0: no piece)
+  int b, hc, g0, n;             // sequence, head chunk, first unit, units of the sequence (0: no piece)
 };
 // Workspace: [2 * CTAs] partials of GHP heads x (D sums, max, total), then [CTAs] Rec, then the share size.
 template <int D, int GHP>
@@ -92,7 +96,7 @@ __device__ __forceinline__ float ex2(float x) {
 // D[16 x 8] += A[16 x 16] * B[16 x 8], fp16 operands, fp32 accumulator.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(   // (not volatile: the compiler may interleave independent chains)
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -119,6 +123,12 @@ __device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
                             *reinterpret_cast<const __half2 *>(&c));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
+// Larger of two pairs of unsigned 16-bit numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // 2^n, n clamped into fp32's normal range.
@@ -128,30 +138,29 @@ __device__ __forceinline__ float q_at(const uint16_t *p, int f16) {
   return f16 ? __half2float(__ushort_as_half(*p)) : __uint_as_float((uint32_t)*p << 16);
 }
 
-// The line of work.  A pair (sequence, head chunk) of n granules takes
-// kPieceCost + n units: opening a piece (staging q, joining the warps) costs
-// about as much as kPieceCost granules do, so shares of many short sequences
+// The line of work.  A pair (sequence, head chunk) of n units takes
+// kPieceCost + n places: opening a piece (staging q, joining the warps) costs
+// about as much as kPieceCost units do, so shares of many short sequences
 // stay level with shares of long ones.  A share that begins inside a pair's first
-// kPieceCost units begins at its granule 0; one that ends there leaves the pair
+// kPieceCost places begins at its unit 0; one that ends there leaves the pair
 // to the next share.
-constexpr int kPieceCost = 8;
+constexpr int kPieceCost = 4;
+constexpr int kUnit = 2 * kv::kTok;   // tokens of a unit
 
 // Where the share of a CTA begins, and its length.
 struct Start {
-  int b, hc, u, pad;             // sequence, head chunk and unit in the pair
-  long long left;                // units of the share; 0: nothing to do
+  int b, hc, u, pad;             // sequence, head chunk and place in the pair
+  long long left;                // places of the share; 0: nothing to do
 };
 
-__device__ __forceinline__ int granules(const Args &a, int b, bool report) {
+// Tokens of sequence b, cut to what its table row can name.
+__device__ __forceinline__ int tokens(const Args &a, int b, bool report) {
   const int len = max(0, __ldg(a.lens + b));
-  int n = len / kv::kTok + (len % kv::kTok != 0);
-  if (n > a.cap_gran) {
-    if (report) atomicOr(&g_device_error, kErrIndex);
-    n = a.cap_gran;
-  }
-  return n;
+  if (len > a.cap && report) atomicOr(&g_device_error, kErrIndex);
+  return min(len, a.cap);
 }
-__device__ __forceinline__ long long units(int n) { return n > 0 ? n + kPieceCost : 0; }
+__device__ __forceinline__ int units(int len) { return len / kUnit + (len % kUnit != 0); }
+__device__ __forceinline__ long long places(int n) { return n > 0 ? n + kPieceCost : 0; }
 
 // Every thread sums a run of the lengths, a scan joins them.
 __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *scan) {
@@ -159,7 +168,7 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
   const int run = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
   long long mine = 0;
-  for (int b = b0; b < b1; b++) mine += units(granules(a, b, blockIdx.x == 0));
+  for (int b = b0; b < b1; b++) mine += places(units(tokens(a, b, blockIdx.x == 0)));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -182,7 +191,7 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
   if (first < total && first >= before && first < before + mine * HC) {
     long long left = first - before;
     for (int b = b0; b < b1; b++) {
-      const long long n = units(granules(a, b, false));
+      const long long n = places(units(tokens(a, b, false)));
       if (left < n * HC) {
         st->b = b;
         st->hc = (int)(left / n);
@@ -197,25 +206,30 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
 }
 
 // A walk over the pieces of a share.  The CTA has one (step 1); each warp has
-// one for its copies, which takes every kWarps-th granule of a piece.
+// one for its copies, which takes every kWarps-th unit of a piece.
 struct Cursor {
-  int b, hc, n;                 // pair, granules of the sequence
-  int g, end;                   // granules [g, end) of the piece are left to this walker
-  long long left;               // units of the share behind this piece
+  int b, hc, n;                 // pair, units of the sequence
+  int g, end;                   // units [g, end) of the piece are left to this walker
+  int len;                      // tokens of the sequence
+  long long left;               // places of the share behind this piece
   const unsigned char *head;    // the pair's head in page 0
   const int32_t *row;           // the sequence's page ids
-  int page;                     // page id of granule g (loaded one granule ahead)
+  int page0, page1;             // page ids of unit g's granules (loaded one unit ahead)
 };
 
 __device__ __forceinline__ void cursor_page(const Args &a, Cursor &c) {
-  if (c.g < c.end) c.page = __ldg(c.row + (c.g >> a.gshift));
+  if (c.g < c.end) {
+    c.page0 = c.page1 = __ldg(c.row + (c.g * 2 >> a.gshift));
+    if (a.gshift == 0 && c.g * kUnit + kv::kTok < c.len) c.page1 = __ldg(c.row + c.g * 2 + 1);
+  }
 }
-// Opens the piece at unit u of (b, hc), skipping empty sequences; false when the share ends in front of it.
+// Opens the piece at place u of (b, hc), skipping empty sequences; false when the share ends in front of it.
 template <int GB>
 __device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int first) {
   c.g = c.end = 0;
   while (c.left > 0 && c.b < a.B) {
-    c.n = granules(a, c.b, false);
+    c.len = tokens(a, c.b, false);
+    c.n = units(c.len);
     if (c.n > 0) {
       const int g = max(0, u - kPieceCost);
       c.left -= max(0, kPieceCost - u);
@@ -248,6 +262,10 @@ template <int GB>
 __device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int first) {
   while (c.g >= c.end && c.left > 0) cursor_next_piece<GB>(a, c, first);
 }
+
+// Resident CTAs an SM that the registers are held to: 16 warps where 128
+// registers a thread hold the state, 8 where it takes more.
+constexpr int min_ctas(int D, int NT) { return D * NT <= 128 ? 4 : 2; }
 
 template <int BITS, int D, int GS, int NT, bool PREC>
 struct Kernel {
@@ -303,7 +321,7 @@ struct Kernel {
   }
 
   // Zeroes the value scales and biases behind the length (the cache may hold
-  // anything there, and 0 * NaN is NaN), before the slot's next copy by a fence.
+  // anything there, and 0 * NaN is NaN); a fence orders it before the slot's next copy.
   static __device__ __forceinline__ void clear_tail(unsigned char *sm, int valid) {
     uint16_t *meta = reinterpret_cast<uint16_t *>(sm + 2 * L.code_bytes + 64 * NG);
     for (int i = threadIdx.x & 31; i < 2 * NG * 16; i += 32)
@@ -312,108 +330,201 @@ struct Kernel {
     __syncwarp();
   }
 
-  // One granule: scores, running max, P, values.  `valid`: its tokens in front of the length.
-  static __device__ __forceinline__ void granule(const unsigned char *sm, int valid, const uint32_t (&qf)[KM][NT][2],
-                                                 const float (&qsum)[NG][NT][2], const float (&sf)[NT][2], State &s) {
+  // Scores of the two granules: 16 tokens x 8 heads a tile, fp32, a group at a
+  // time.  The granules' MMA chains are independent and stand side by side (an
+  // MMA's result takes 25 cycles, its issue slot 8).
+  static __device__ __forceinline__ void scores(const unsigned char *sm, const uint32_t (&qf)[KM][NT][2],
+                                                const float (&qsum)[NG][NT][2], float (&sc)[2][NT][4]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    // ---- scores: 16 tokens x 8 heads, fp32, a group at a time
-    float sc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; t++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) sc[t][j] = 0.0f;
-    uint32_t km[2][NG];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const uint32_t *p = reinterpret_cast<const uint32_t *>(sm + 2 * L.code_bytes) + (r + 8 * h) * NG;
-      if constexpr (NG % 4 == 0) {
-#pragma unroll
-        for (int g = 0; g < NG; g += 4) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(p + g);
-          km[h][g] = u.x; km[h][g + 1] = u.y; km[h][g + 2] = u.z; km[h][g + 3] = u.w;
-        }
-      } else if constexpr (NG == 2) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        km[h][0] = u.x; km[h][1] = u.y;
-      } else {
-        km[h][0] = p[0];
-      }
-    }
     constexpr int WG = GS * BITS / 128;             // words (of a lane's row) a group
-    float ga[NT][4];
+    const unsigned char *meta = sm + 2 * L.code_bytes + r * NG * 4;
+    const unsigned char *row = sm + (r * 4 + c) * L.VW * 4;
+    float ga[2][NT][4];
 #pragma unroll
     for (int a = 0; a < L.NW / (4 * L.VW); a++) {
-      uint32_t w[2][4];
+      uint32_t w[2][2][4];                          // [granule][row r, r + 8][word]
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(sm) + ((a * 16 + r + 8 * h) * 4 + c) * L.VW;
-        if constexpr (L.VW == 4) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(p);
-          w[h][0] = u.x; w[h][1] = u.y; w[h][2] = u.z; w[h][3] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2 *>(p);
-          w[h][0] = u.x; w[h][1] = u.y;
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          const unsigned char *p = row + h * GB + (a * 16 + 8 * k) * 4 * L.VW * 4;
+          if constexpr (L.VW == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[h][k][0] = u.x; w[h][k][1] = u.y; w[h][k][2] = u.z; w[h][k][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[h][k][0] = u.x; w[h][k][1] = u.y;
+          }
         }
-      }
 #pragma unroll
       for (int v = 0; v < L.VW; v++) {
         const int i = a * L.VW + v;                 // word column 4 i + c of the row
         if (i % WG == 0)
 #pragma unroll
-          for (int t = 0; t < NT; t++)
+          for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) ga[t][j] = 0.0f;
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+              for (int j = 0; j < 4; j++) ga[h][t][j] = 0.0f;
         if constexpr (BITS == 4) {
-          const uint32_t x0 = w[0][v], x1 = w[1][v], y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
-          for (int t = 0; t < NT; t++) {
-            mma(ga[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[2 * i][t][0],
-                qf[2 * i][t][1]);
-            mma(ga[t], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qf[2 * i + 1][t][0],
-                qf[2 * i + 1][t][1]);
-          }
+          for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const uint32_t x0 = w[h][0][v] >> (8 * k), x1 = w[h][1][v] >> (8 * k);
+#pragma unroll
+              for (int t = 0; t < NT; t++)
+                mma(ga[h][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                    qf[2 * i + k][t][0], qf[2 * i + k][t][1]);
+            }
         } else {
-          const uint32_t x0 = w[0][v], x1 = w[1][v];
 #pragma unroll
-          for (int t = 0; t < NT; t++)
-            mma(ga[t], x0 & 0x00ff00ffu, x1 & 0x00ff00ffu, (x0 >> 8) & 0x00ff00ffu, (x1 >> 8) & 0x00ff00ffu,
-                qf[i][t][0], qf[i][t][1]);
+          for (int h = 0; h < 2; h++) {
+            const uint32_t x0 = w[h][0][v], x1 = w[h][1][v];
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+              mma(ga[h][t], x0 & 0x00ff00ffu, x1 & 0x00ff00ffu, (x0 >> 8) & 0x00ff00ffu, (x1 >> 8) & 0x00ff00ffu,
+                  qf[i][t][0], qf[i][t][1]);
+          }
         }
         if (i % WG == WG - 1) {
           const int g = i / WG;
 #pragma unroll
-          for (int t = 0; t < NT; t++) {
-            sc[t][0] = fmaf(ga[t][0], bf_lo(km[0][g]), fmaf(qsum[g][t][0], bf_hi(km[0][g]), sc[t][0]));
-            sc[t][1] = fmaf(ga[t][1], bf_lo(km[0][g]), fmaf(qsum[g][t][1], bf_hi(km[0][g]), sc[t][1]));
-            sc[t][2] = fmaf(ga[t][2], bf_lo(km[1][g]), fmaf(qsum[g][t][0], bf_hi(km[1][g]), sc[t][2]));
-            sc[t][3] = fmaf(ga[t][3], bf_lo(km[1][g]), fmaf(qsum[g][t][1], bf_hi(km[1][g]), sc[t][3]));
-          }
+          for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+              const uint32_t m = *reinterpret_cast<const uint32_t *>(meta + h * GB + (8 * k * NG + g) * 4);
+              const float ms = bf_lo(m), mb = bf_hi(m);
+#pragma unroll
+              for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                  const float base = g == 0 ? qsum[g][t][e] * mb : fmaf(qsum[g][t][e], mb, sc[h][t][2 * k + e]);
+                  sc[h][t][2 * k + e] = fmaf(ga[h][t][2 * k + e], ms, base);
+                }
+            }
         }
       }
     }
+  }
+
+  // Values of a granule: sum of P * (bias + Z scale) a group, and P * scale against the codes.
+  static __device__ __forceinline__ void values(const unsigned char *sm, const uint32_t (&ph)[NT][2],
+                                                const uint32_t (&pl)[NT][2], State &s) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG + c * 8, *vb = vs + 32 * NG;
+    {
+      // one MMA: row g of A = group g's (lane r < NG)
+      const int g = r % NG;
+      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32), b = *reinterpret_cast<const uint2 *>(vb + g * 32);
+      const float z = (float)(1 << (BITS - 1)) * s.fb;
+      uint32_t a0 = pack_h2(fmaf(bf_lo(u.x), z, bf_lo(b.x) * s.fb), fmaf(bf_hi(u.x), z, bf_hi(b.x) * s.fb));
+      uint32_t a2 = pack_h2(fmaf(bf_lo(u.y), z, bf_lo(b.y) * s.fb), fmaf(bf_hi(u.y), z, bf_hi(b.y) * s.fb));
+      if (NG < 8 && r >= NG) a0 = a2 = 0u;
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        mma(s.bacc[t], a0, 0u, a2, 0u, ph[t][0], ph[t][1]);
+        if constexpr (PREC) mma(s.bacc[t], a0, 0u, a2, 0u, pl[t][0], pl[t][1]);
+      }
+    }
+    // !PREC: subnormal codes, and -Z, -16 Z (4-bit) times 2^-24 for the centring MMA
+    constexpr uint32_t kC = BITS == 4 ? 0x80088008u : 0x80808080u, kC16 = 0x80808080u;
+    // PREC: 1024 + code, and -(1024 + Z), -(1024 + 16 Z): the centred codes as normal numbers
+    constexpr uint32_t kM = BITS == 4 ? 0xe408e408u : 0xe480e480u, kM16 = 0xe480e480u;
+    const uint4 *vc = reinterpret_cast<const uint4 *>(sm + L.code_bytes) + lane;
+    uint32_t b[NG][NT][2];
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32);
+      const float f = s.fs[g];
+      const uint32_t s0 = pack_h2(bf_lo(u.x) * f, bf_hi(u.x) * f), s1 = pack_h2(bf_lo(u.y) * f, bf_hi(u.y) * f);
+      uint32_t bl[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        b[g][t][0] = hmul2u(ph[t][0], s0);
+        b[g][t][1] = hmul2u(ph[t][1], s1);
+        if constexpr (PREC) {
+          bl[t][0] = hfma2u(pl[t][0], s0, hfma2u(ph[t][0], s0, b[g][t][0] ^ 0x80008000u));
+          bl[t][1] = hfma2u(pl[t][1], s1, hfma2u(ph[t][1], s1, b[g][t][1] ^ 0x80008000u));
+        }
+      }
+#pragma unroll
+      for (int j = g * GS / DB; j < (g + 1) * GS / DB; j++) {
+        const uint4 q4 = vc[(j / 2) * 32];           // two blocks share a 16-byte load
+        const uint32_t x = j % 2 ? q4.z : q4.x, w = j % 2 ? q4.w : q4.y;
+        constexpr uint32_t m0 = BITS == 4 ? 0x000f000fu : 0x00ff00ffu, m1 = BITS == 4 ? 0x00f000f0u : 0x00ff00ffu;
+        constexpr uint32_t or_ = PREC ? 0x64006400u : 0u;
+        const uint32_t x8 = x >> 8, w8 = w >> 8;
+        uint32_t f4[2][4] = {{(x & m0) | or_, ((BITS == 4 ? x : x8) & m1) | or_, (w & m0) | or_, ((BITS == 4 ? w : w8) & m1) | or_},
+                             {(x8 & m0) | or_, (x8 & m1) | or_, (w8 & m0) | or_, (w8 & m1) | or_}};
+        if constexpr (PREC)
+#pragma unroll
+          for (int k = 0; k < MPB; k++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) f4[k][i] = hadd2u(f4[k][i], i % 2 ? kM16 : kM);
+#pragma unroll
+        for (int k = 0; k < MPB; k++)
+#pragma unroll
+          for (int t = 0; t < NT; t++) {
+            float(&acc)[4] = s.acc[MPB * j + k][t];
+            mma(acc, f4[k][0], f4[k][1], f4[k][2], f4[k][3], b[g][t][0], b[g][t][1]);
+            if constexpr (PREC) mma(acc, f4[k][0], f4[k][1], f4[k][2], f4[k][3], bl[t][0], bl[t][1]);
+          }
+      }
+    }
+    if constexpr (!PREC)                             // minus Z * sum of P * scale
+#pragma unroll
+      for (int j = 0; j < VB * MPB; j++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          constexpr int per = VB * MPB / NG;
+          mma(s.acc[j][t], kC, kC16, kC, kC16, b[j / per][t][0], b[j / per][t][1]);
+        }
+  }
+
+  // One unit (two granules): scores, running max, P, values of its tokens lo ..
+  // valid - 1, lo 0 or 16 and below valid.  Of the others, scores are masked and
+  // value scales and biases must be zero (clear_tail).
+  static __device__ __forceinline__ void unit(const unsigned char *sm, int lo, int valid, const uint32_t (&qf)[KM][NT][2],
+                                              const float (&qsum)[NG][NT][2], const float (&sf)[NT][2], State &s) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8: t0, t0 + 2
+    float sc[2][NT][4], y[2][NT][4];
+    scores(sm, qf, qsum, sc);
     // ---- running max: moved only when a P would pass 2^14
-    float y[NT][4], top = -INFINITY;
+    auto exponents = [&]() {
 #pragma unroll
-    for (int t = 0; t < NT; t++)
+      for (int h = 0; h < 2; h++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) y[t][j] = fmaf(sc[t][j], sf[t][j & 1], -s.m10[t][j & 1]);
-    const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8
-    if (valid < kv::kTok)                           // the sequence's last granule
+        for (int t = 0; t < NT; t++)
 #pragma unroll
-      for (int t = 0; t < NT; t++)
+          for (int j = 0; j < 4; j++) y[h][t][j] = fmaf(sc[h][t][j], sf[t][j & 1], -s.m10[t][j & 1]);
+      if (lo > 0 || valid < kUnit)                  // the sequence's last unit, or a page is missing
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-          if (t0 + j / 2 * 2 >= valid) y[t][j] = -INFINITY;
+        for (int h = 0; h < 2; h++)
 #pragma unroll
-    for (int t = 0; t < NT; t++) top = fmaxf(fmaxf(fmaxf(y[t][0], y[t][1]), fmaxf(y[t][2], y[t][3])), top);
+          for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              if (16 * h < lo || 16 * h + t0 + j / 2 * 2 >= valid) y[h][t][j] = -INFINITY;
+    };
+    exponents();
+    float top = y[0][0][0];
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int t = 0; t < NT; t++) top = fmaxf(fmaxf(fmaxf(y[h][t][0], y[h][t][1]), fmaxf(y[h][t][2], y[h][t][3])), top);
     if (__any_sync(kFull, top > kLogPMax)) {
-      const bool in0 = t0 < valid, in1 = t0 + 2 < valid;
 #pragma unroll
       for (int t = 0; t < NT; t++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          const float a0 = in0 ? sc[t][e] * sf[t][e] : -INFINITY, a1 = in1 ? sc[t][e + 2] * sf[t][e] : -INFINITY;
-          float mx = fmaxf(a0, a1);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+              if (16 * h >= lo && 16 * h + t0 + 2 * k < valid) mx = fmaxf(mx, sc[h][t][e + 2 * k] * sf[t][e]);
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
@@ -427,41 +538,48 @@ struct Kernel {
             s.acc[i][t][e] *= f;
             s.acc[i][t][e + 2] *= f;
           }
-          y[t][e] = in0 ? fmaf(sc[t][e], sf[t][e], -m) : -INFINITY;
-          y[t][e + 2] = in1 ? fmaf(sc[t][e + 2], sf[t][e], -m) : -INFINITY;
         }
+      exponents();
     }
     // ---- P, rounded to fp16 and transposed to the B operand: k = token, n = head
-    uint32_t ph[NT][2], pl[NT][2];
+    uint32_t ph[2][NT][2], pl[2][NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-      float p[4];
+    for (int h = 0; h < 2; h++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        p[j] = ex2(y[t][j]);
-        s.l[t][j & 1] += p[j];
+      for (int t = 0; t < NT; t++) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          p[j] = ex2(y[h][t][j]);
+          s.l[t][j & 1] += p[j];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          const uint32_t u = pack_h2(p[2 * k], p[2 * k + 1]);
+          if constexpr (PREC) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+            pl[h][t][k] = transpose8x8(pack_h2(p[2 * k] - f.x, p[2 * k + 1] - f.y));
+          }
+          ph[h][t][k] = transpose8x8(u);
+        }
       }
+    // ---- the groups' powers of two: lane r checks group r % NG
+    {
+      const int g = r % NG;
+      const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG + c * 8 + g * 32;
+      uint32_t su = 0, bu = 0;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const uint32_t u = pack_h2(p[2 * h], p[2 * h + 1]);
-        if constexpr (PREC) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-          pl[t][h] = transpose8x8(pack_h2(p[2 * h] - f.x, p[2 * h + 1] - f.y));
+          const uint2 u = *reinterpret_cast<const uint2 *>(vs + h * GB);
+          const uint2 b = *reinterpret_cast<const uint2 *>(vs + h * GB + 32 * NG);
+          su = max_u16x2(su, max_u16x2(u.x, u.y));
+          bu = max_u16x2(bu, max_u16x2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu));
         }
-        ph[t][h] = transpose8x8(u);
-      }
-    }
-    // ---- value scales and biases of tokens 4c .. 4c+3
-    const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG + c * 8, *vb = vs + 32 * NG;
-    {
-      // the groups' powers of two: lane r checks (and for r < NG holds the biases of) group r % NG
-      const int g = r % NG;
-      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32), b = *reinterpret_cast<const uint2 *>(vb + g * 32);
-      const uint32_t su = __vmaxu2(u.x, u.y) & 0x7fff7fffu, bu = __vmaxu2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu);
-      const uint32_t sm_ = max(su & 0xffffu, su >> 16), bm = max(bu & 0xffffu, bu >> 16);
-      if (__any_sync(kFull, (sm_ > s.lim_s) | (bm > s.lim_b))) {
+      su &= 0x7fff7fffu;
+      const uint32_t s1 = max(su & 0xffffu, su >> 16), b1 = max(bu & 0xffffu, bu >> 16);
+      if (__any_sync(kFull, (s1 > s.lim_s) | (b1 > s.lim_b))) {
         // exponents that hold scale * 2^BITS and |bias| below 2^E
-        const int need = min(120, max((int)(sm_ >> 7) - 126 + BITS, (int)(bm >> 7) - 126));
+        const int need = min(120, max((int)(s1 >> 7) - 126 + BITS, (int)(b1 >> 7) - 126));
 #pragma unroll
         for (int i = 0; i < NG; i++) {
           int e = __reduce_max_sync(kFull, g == i ? need : -126);
@@ -487,67 +605,9 @@ struct Kernel {
           }
         }
       }
-      // sum of P * (bias + Z scale): one MMA, row g of A = group g's biases
-      const float z = (float)(1 << (BITS - 1)) * s.fb;
-      uint32_t a0 = pack_h2(fmaf(bf_lo(u.x), z, bf_lo(b.x) * s.fb), fmaf(bf_hi(u.x), z, bf_hi(b.x) * s.fb));
-      uint32_t a2 = pack_h2(fmaf(bf_lo(u.y), z, bf_lo(b.y) * s.fb), fmaf(bf_hi(u.y), z, bf_hi(b.y) * s.fb));
-      if (NG < 8 && r >= NG) a0 = a2 = 0u;
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        mma(s.bacc[t], a0, 0u, a2, 0u, ph[t][0], ph[t][1]);
-        if constexpr (PREC) mma(s.bacc[t], a0, 0u, a2, 0u, pl[t][0], pl[t][1]);
-      }
     }
-    // ---- values: a group at a time, P * scale against the centred codes
-    constexpr uint32_t kC = BITS == 4 ? 0x80088008u : 0x80808080u;     // -Z * 2^-24 in both halves
-    constexpr uint32_t kC16 = 0x80808080u;                             // -16 Z * 2^-24 (4-bit)
-    const uint4 *vc = reinterpret_cast<const uint4 *>(sm + L.code_bytes) + lane;
-#pragma unroll
-    for (int g = 0; g < NG; g++) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32);
-      const float f = s.fs[g];
-      const uint32_t s0 = pack_h2(bf_lo(u.x) * f, bf_hi(u.x) * f), s1 = pack_h2(bf_lo(u.y) * f, bf_hi(u.y) * f);
-      uint32_t b[NT][2], bl[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        b[t][0] = hmul2u(ph[t][0], s0);
-        b[t][1] = hmul2u(ph[t][1], s1);
-        if constexpr (PREC) {
-          bl[t][0] = hfma2u(pl[t][0], s0, hfma2u(ph[t][0], s0, b[t][0] ^ 0x80008000u));
-          bl[t][1] = hfma2u(pl[t][1], s1, hfma2u(ph[t][1], s1, b[t][1] ^ 0x80008000u));
-        }
-      }
-#pragma unroll
-      for (int j = g * GS / DB; j < (g + 1) * GS / DB; j++) {
-        // two blocks share a 16-byte load; the compiler keeps the second half
-        const uint4 q4 = vc[(j / 2) * 32];
-        const uint32_t x = j % 2 ? q4.z : q4.x, w = j % 2 ? q4.w : q4.y;
-        if constexpr (BITS == 4) {
-          const uint32_t x8 = x >> 8, w8 = w >> 8;
-          const uint32_t a0 = hadd2u(x & 0x000f000fu, kC), a1 = hadd2u(x & 0x00f000f0u, kC16);
-          const uint32_t a2 = hadd2u(w & 0x000f000fu, kC), a3 = hadd2u(w & 0x00f000f0u, kC16);
-          const uint32_t c0 = hadd2u(x8 & 0x000f000fu, kC), c1 = hadd2u(x8 & 0x00f000f0u, kC16);
-          const uint32_t c2 = hadd2u(w8 & 0x000f000fu, kC), c3 = hadd2u(w8 & 0x00f000f0u, kC16);
-#pragma unroll
-          for (int t = 0; t < NT; t++) {
-            mma(s.acc[2 * j][t], a0, a1, a2, a3, b[t][0], b[t][1]);
-            mma(s.acc[2 * j + 1][t], c0, c1, c2, c3, b[t][0], b[t][1]);
-            if constexpr (PREC) {
-              mma(s.acc[2 * j][t], a0, a1, a2, a3, bl[t][0], bl[t][1]);
-              mma(s.acc[2 * j + 1][t], c0, c1, c2, c3, bl[t][0], bl[t][1]);
-            }
-          }
-        } else {
-          const uint32_t a0 = hadd2u(x & 0x00ff00ffu, kC), a1 = hadd2u((x >> 8) & 0x00ff00ffu, kC);
-          const uint32_t a2 = hadd2u(w & 0x00ff00ffu, kC), a3 = hadd2u((w >> 8) & 0x00ff00ffu, kC);
-#pragma unroll
-          for (int t = 0; t < NT; t++) {
-            mma(s.acc[j][t], a0, a1, a2, a3, b[t][0], b[t][1]);
-            if constexpr (PREC) mma(s.acc[j][t], a0, a1, a2, a3, bl[t][0], bl[t][1]);
-          }
-        }
-      }
-    }
+    values(sm, ph[0], pl[0], s);
+    values(sm + GB, ph[1], pl[1], s);
   }
 
   // Writes this warp's sums (value units, over 2^kLogP) and max / total to the join buffer.
@@ -572,7 +632,7 @@ struct Kernel {
           const float fe = p2(s.E[g]);
 #pragma unroll
           for (int j = g * GS / DB; j < (g + 1) * GS / DB; j++) {
-            constexpr float f1 = (float)(1 << (24 - BITS));
+            constexpr float f1 = PREC ? 1.0f / (1 << BITS) : (float)(1 << (24 - BITS));
             if constexpr (BITS == 4) {
               float4 v;
               v.x = fmaf(s.acc[2 * j][t][e], f1, bias) * fe;
@@ -610,7 +670,7 @@ __device__ __forceinline__ float lse_of(float m10, float l) {
 }
 
 template <int BITS, int D, int GS, int NT, bool PREC>
-__global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
+__global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const Args a) {
   using K = Kernel<BITS, D, GS, NT, PREC>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[kWarps * 8];
@@ -619,7 +679,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   float *join = reinterpret_cast<float *>(smem_raw);                         // [warp][GHP][SROW], then [warp][GHP][2]
   float *join_ml = join + kWarps * K::GHP * K::SROW;
-  unsigned char *ring = smem_raw + ((K::kJoin + 15) & ~15) + warp * a.depth * K::GB;
+  unsigned char *ring = smem_raw + ((K::kJoin + 15) & ~15) + warp * a.depth * 2 * K::GB;
   uint64_t *bar = bars + warp * 8;
 
   if (lane == 0)
@@ -631,7 +691,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
 
   // rows without a token: zeros, and minus infinity for the log-sum-exp
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (granules(a, b, false) == 0) {
+    if (tokens(a, b, false) == 0) {
       const int64_t row = (int64_t)b * a.H * a.G;
       for (int i = tid; i < a.H * a.G * D; i += kThreads) a.out[row * D + i] = 0;
       if (a.lse)
@@ -653,22 +713,35 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
   if (tid == 0) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
 
   uint32_t filled = 0, phase = 0;     // slots with a copy, parity of each slot's next wait
+  uint32_t lack0 = 0, lack1 = 0;      // slots without their first / second granule
   int slot_in = 0, slot_out = 0;
   bool dead = false;
   const int64_t page_bytes = ((int64_t)a.H << a.gshift) * K::GB;
-  auto issue = [&]() {                // the cursor's granule into slot_in
+  auto issue = [&]() {                // the cursor's unit into slot_in
     if (cp.g >= cp.end) return;
-    const int page = cp.page;
-    if (page >= 0 && page < a.pages) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar + slot_in, K::GB);
-        bulk_load(ring + slot_in * K::GB, cp.head + page * page_bytes + (cp.g & ((1 << a.gshift) - 1)) * K::GB, K::GB,
-                  bar + slot_in);
+    // the granules to copy: the second only where a token of it is in front of the length (its page may not
+    // exist), neither where its page id is outside the cache (left out and reported)
+    const bool two = cp.g * kUnit + kv::kTok < cp.len;
+    const bool ok0 = (uint32_t)cp.page0 < (uint32_t)a.pages, ok1 = two && (uint32_t)cp.page1 < (uint32_t)a.pages;
+    if (lane == 0) {
+      unsigned char *dst = ring + slot_in * 2 * K::GB;
+      const unsigned char *src = cp.head + cp.page0 * page_bytes + (cp.g * 2 & ((1 << a.gshift) - 1)) * K::GB;
+      if (a.gshift != 0) {                       // both in one page
+        if (ok0) {
+          mbar_arrive_expect_tx(bar + slot_in, two ? 2 * K::GB : K::GB);
+          bulk_load(dst, src, two ? 2 * K::GB : K::GB, bar + slot_in);
+        }
+      } else if (ok0 || ok1) {
+        mbar_arrive_expect_tx(bar + slot_in, ok0 && ok1 ? 2 * K::GB : K::GB);
+        if (ok0) bulk_load(dst, src, K::GB, bar + slot_in);
+        if (ok1) bulk_load(dst + K::GB, cp.head + cp.page1 * page_bytes, K::GB, bar + slot_in);
       }
-      filled |= 1u << slot_in;
-    } else if (lane == 0) {
-      atomicOr(&g_device_error, kErrIndex);      // the granule is left out
+      if (!ok0 || (two && !ok1)) atomicOr(&g_device_error, kErrIndex);
     }
+    const uint32_t bit = 1u << slot_in;
+    filled = ok0 || ok1 ? filled | bit : filled & ~bit;
+    lack0 = ok0 ? lack0 & ~bit : lack0 | bit;
+    lack1 = ok1 ? lack1 & ~bit : lack1 | bit;
     slot_in = slot_in + 1 == a.depth ? 0 : slot_in + 1;
     cp.g += kWarps;
     cursor_page(a, cp);
@@ -756,16 +829,20 @@ __global__ void __launch_bounds__(kThreads) k_attn_decode(const Args a) {
       }
     }
     K::reset(s);
-    const int len = min(max(0, __ldg(a.lens + pc.b)), a.cap_gran * kv::kTok);
 
-    // ---- this warp's granules of the piece
+    // ---- this warp's units of the piece
     for (int g = g_first + warp; g < pc.end; g += kWarps) {
       if ((filled >> slot_out & 1u) && !dead) {
         if (mbar_wait(bar + slot_out, phase >> slot_out & 1u)) {
-          unsigned char *gran = ring + slot_out * K::GB;
-          const int valid = len - g * kv::kTok;
-          if (valid < kv::kTok) K::clear_tail(gran, valid);
-          K::granule(gran, valid, qf, qsum, sf, s);
+          unsigned char *sm = ring + slot_out * 2 * K::GB;
+          int lo = 0, valid = pc.len - g * kUnit;
+          if (lack0 >> slot_out & 1u) lo = kv::kTok;
+          if (lack1 >> slot_out & 1u) valid = min(valid, kv::kTok);
+          if (lo > 0 || valid < kUnit) {
+            K::clear_tail(sm, lo > 0 ? 0 : valid);
+            K::clear_tail(sm + K::GB, valid - kv::kTok);
+          }
+          K::unit(sm, lo, valid, qf, qsum, sf, s);
           phase ^= 1u << slot_out;
           filled &= ~(1u << slot_out);
         } else {
@@ -933,8 +1010,8 @@ attn::Args attn_args(const AttnCall &c) {
   a.GH = (a.G + a.chunks - 1) / a.chunks;
   int gpp = (int)(c.cache.page_size / kv::kTok);
   while (gpp >>= 1) a.gshift++;
-  const int64_t cap = c.max_pages * (c.cache.page_size / kv::kTok);
-  a.cap_gran = (int)(cap < (1 << 27) ? cap : (1 << 27) - 1);   // (16 times this stays an int)
+  const int64_t cap = c.max_pages * c.cache.page_size;
+  a.cap = (int)(cap < 0x7fffff00 ? cap : 0x7fffff00);          // (a whole number of units)
   a.min_per = attn::kPieceCost + attn::kWarps;
   a.f16 = c.f16;
   a.scale_log2 = c.scale * 1.4426950408889634f;
@@ -948,9 +1025,10 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   auto kern = attn::k_attn_decode<BITS, D, GS, NT, PREC>;
   const size_t join = (K::kJoin + 15) & ~15;
   // ring depth: what lets four CTAs share an SM (227 KB less 1 KB a CTA), at least 2 slots, at most 6
-  int depth = (int)((227 * 1024 / 4 - 1536 - join) / ((size_t)attn::kWarps * K::GB));
-  depth = join + 1536 > 227 * 1024 / 4 ? 2 : (depth < 2 ? 2 : (depth > 6 ? 6 : depth));
-  const size_t smem = join + (size_t)attn::kWarps * depth * K::GB;
+  constexpr size_t slot = (size_t)attn::kWarps * 2 * K::GB;
+  int depth = join + 1536 < 227 * 1024 / 4 ? (int)((227 * 1024 / 4 - 1536 - join) / slot) : 0;
+  depth = depth < 2 ? 2 : (depth > 6 ? 6 : depth);
+  const size_t smem = join + depth * slot;
   AttnSetup su;
   gwb_status s = attn_setup(reinterpret_cast<const void *>(kern), smem, attn::kThreads, &su);
   if (s != GWB_OK) return s;
