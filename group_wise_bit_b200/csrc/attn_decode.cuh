@@ -101,6 +101,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// D = A * B (no registers to clear).
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -280,26 +287,31 @@ struct Kernel {
   static constexpr int SROW = D + 4;                      // floats of a head's row in the join buffer
   static constexpr int kJoin = kWarps * GHP * (SROW + 2) * 4;
 
+  // Pairs of tokens whose value scale and bias a lane converts a unit: word lane + 32 k of the
+  // unit's 16 NG, of granule i / (8 NG), group i / 8 % NG.
+  static constexpr int MW = (NG + 1) / 2;
   // One warp's state of the current piece.
   struct State {
     float acc[VB * MPB][NT][4];
-    float bacc[NT][4];            // row r < NG: sum of P * (bias + Z scale) of group r
+    float bacc[NT][4];            // [0], [1] of row r < NG: sum of P * (bias + Z scale) of group r
     float m10[NT][2], l[NT][2];   // running max (log2, minus kLogP) and this lane's total, heads 8 nt + 2c, +1
-    int E[NG];                    // value scales and biases are held over 2^E ...
-    float fs[NG];                 // ... and this is 2^(BITS - E)
-    float fb;                     // 2^-E of this lane's group r % NG, and the largest scale and |bias|
-    uint32_t lim_s, lim_b;        // (bf16 bits) that 2^E holds
+    int E[NG];                    // value scales and biases are held over 2^E
+    float fs[MW], fb[MW];         // 2^(BITS - E), 2^-E of the groups this lane converts (convert_meta),
+    uint32_t lim_s[MW], lim_b[MW];   // and the largest scale and |bias| (bf16 bits, in both halves) that 2^E holds
   };
+  static constexpr int kMeta = 128 * NG;              // bytes of a warp's converted scales and biases
+  static __device__ __forceinline__ int meta_group(int k) { return (((threadIdx.x & 31) + 32 * k) / 8) % NG; }
 
-  // Scale bits below 2^(E - BITS) and |bias| bits below 2^E fit.
-  static __device__ __forceinline__ void set_exponent(State &s, int g, int e, bool own) {
+  static __device__ __forceinline__ void set_exponent(State &s, int g, int e) {
     s.E[g] = e;
-    s.fs[g] = p2(BITS - e);
-    if (own) {
-      s.fb = p2(-e);
-      s.lim_s = (uint32_t)(max(0, 127 + e - BITS) << 7) - 1u;
-      s.lim_b = (uint32_t)((127 + e) << 7) - 1u;
-    }
+#pragma unroll
+    for (int k = 0; k < MW; k++)
+      if (meta_group(k) == g) {
+        s.fs[k] = p2(BITS - e);
+        s.fb[k] = p2(-e);
+        s.lim_s[k] = ((uint32_t)(max(0, 127 + e - BITS) << 7) - 1u) * 0x10001u;
+        s.lim_b[k] = ((uint32_t)((127 + e) << 7) - 1u) * 0x10001u;
+      }
   }
 
   static __device__ __forceinline__ void reset(State &s) {
@@ -317,7 +329,7 @@ struct Kernel {
       s.l[t][0] = s.l[t][1] = 0.0f;
     }
 #pragma unroll
-    for (int g = 0; g < NG; g++) set_exponent(s, g, -100, g == ((threadIdx.x & 31) >> 2) % NG);
+    for (int g = 0; g < NG; g++) set_exponent(s, g, -100);
   }
 
   // Zeroes the value scales and biases behind the length (the cache may hold
@@ -339,7 +351,9 @@ struct Kernel {
     constexpr int WG = GS * BITS / 128;             // words (of a lane's row) a group
     const unsigned char *meta = sm + 2 * L.code_bytes + r * NG * 4;
     const unsigned char *row = sm + (r * 4 + c) * L.VW * 4;
+    constexpr int MV = NG < 4 ? NG : 4;             // groups of a meta load
     float ga[2][NT][4];
+    uint32_t km[2][2][MV];
 #pragma unroll
     for (int a = 0; a < L.NW / (4 * L.VW); a++) {
       uint32_t w[2][2][4];                          // [granule][row r, r + 8][word]
@@ -359,32 +373,30 @@ struct Kernel {
 #pragma unroll
       for (int v = 0; v < L.VW; v++) {
         const int i = a * L.VW + v;                 // word column 4 i + c of the row
-        if (i % WG == 0)
-#pragma unroll
-          for (int h = 0; h < 2; h++)
-#pragma unroll
-            for (int t = 0; t < NT; t++)
-#pragma unroll
-              for (int j = 0; j < 4; j++) ga[h][t][j] = 0.0f;
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int k = 0; k < 2; k++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
               const uint32_t x0 = w[h][0][v] >> (8 * k), x1 = w[h][1][v] >> (8 * k);
+              const uint32_t m0 = 0x000f000fu, m1 = 0x00f000f0u;
 #pragma unroll
-              for (int t = 0; t < NT; t++)
-                mma(ga[h][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
-                    qf[2 * i + k][t][0], qf[2 * i + k][t][1]);
+              for (int t = 0; t < NT; t++) {
+                const uint32_t(&q)[2] = qf[2 * i + k][t];
+                if (i % WG == 0 && k == 0) mma0(ga[h][t], x0 & m0, x1 & m0, x0 & m1, x1 & m1, q[0], q[1]);
+                else mma(ga[h][t], x0 & m0, x1 & m0, x0 & m1, x1 & m1, q[0], q[1]);
+              }
             }
         } else {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
-            const uint32_t x0 = w[h][0][v], x1 = w[h][1][v];
+            const uint32_t x0 = w[h][0][v], x1 = w[h][1][v], m0 = 0x00ff00ffu;
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-              mma(ga[h][t], x0 & 0x00ff00ffu, x1 & 0x00ff00ffu, (x0 >> 8) & 0x00ff00ffu, (x1 >> 8) & 0x00ff00ffu,
-                  qf[i][t][0], qf[i][t][1]);
+            for (int t = 0; t < NT; t++) {
+              const uint32_t(&q)[2] = qf[i][t];
+              if (i % WG == 0) mma0(ga[h][t], x0 & m0, x1 & m0, (x0 >> 8) & m0, (x1 >> 8) & m0, q[0], q[1]);
+              else mma(ga[h][t], x0 & m0, x1 & m0, (x0 >> 8) & m0, (x1 >> 8) & m0, q[0], q[1]);
+            }
           }
         }
         if (i % WG == WG - 1) {
@@ -393,7 +405,19 @@ struct Kernel {
           for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int k = 0; k < 2; k++) {
-              const uint32_t m = *reinterpret_cast<const uint32_t *>(meta + h * GB + (8 * k * NG + g) * 4);
+              if (g % MV == 0) {
+                const unsigned char *p = meta + h * GB + (8 * k * NG + g) * 4;
+                if constexpr (MV == 4) {
+                  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+                  km[h][k][0] = u.x; km[h][k][1] = u.y; km[h][k][2] = u.z; km[h][k][3] = u.w;
+                } else if constexpr (MV == 2) {
+                  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                  km[h][k][0] = u.x; km[h][k][1] = u.y;
+                } else {
+                  km[h][k][0] = *reinterpret_cast<const uint32_t *>(p);
+                }
+              }
+              const uint32_t m = km[h][k][g % MV];
               const float ms = bf_lo(m), mb = bf_hi(m);
 #pragma unroll
               for (int t = 0; t < NT; t++)
@@ -408,23 +432,89 @@ struct Kernel {
     }
   }
 
+  // The unit's value scales (over 2^(E - BITS)) and centred biases (bias + Z scale, over 2^E) as fp16, each
+  // converted once into the warp's buffer: [granule][group][c][bias, scale of tokens 4c, 4c + 1; bias, scale of
+  // 4c + 2, 4c + 3], an A operand as it stands: rows r are the biases' sums, rows r + 8 (the scales') are not used.
+  // Moves a group's power of two first where one of them does not fit.
+  static __device__ __forceinline__ void convert_meta(const unsigned char *sm, unsigned char *buf, State &s) {
+    const int lane = threadIdx.x & 31;
+    uint32_t su[MW], bu[MW];
+    bool over = false;
+#pragma unroll
+    for (int k = 0; k < MW; k++) {
+      const int i = lane + 32 * k, h = i / (8 * NG), gp = i % (8 * NG);
+      su[k] = bu[k] = 0;
+      if (NG > 1 || lane < 16) {
+        const unsigned char *p = sm + h * GB + 2 * L.code_bytes + 64 * NG + gp * 4;
+        su[k] = *reinterpret_cast<const uint32_t *>(p);
+        bu[k] = *reinterpret_cast<const uint32_t *>(p + 32 * NG);
+      }
+      over |= max_u16x2(su[k], s.lim_s[k]) != s.lim_s[k];
+      over |= max_u16x2(bu[k] & 0x7fff7fffu, s.lim_b[k]) != s.lim_b[k];
+    }
+    if (__any_sync(kFull, over)) {
+      // exponents that hold scale * 2^BITS and |bias| below 2^E
+      int need[MW];
+#pragma unroll
+      for (int k = 0; k < MW; k++) {
+        const uint32_t u = su[k] & 0x7fff7fffu, v = bu[k] & 0x7fff7fffu;
+        const uint32_t s1 = max(u & 0xffffu, u >> 16), b1 = max(v & 0xffffu, v >> 16);
+        need[k] = min(120, max((int)(s1 >> 7) - 126 + BITS, (int)(b1 >> 7) - 126));
+      }
+#pragma unroll
+      for (int i = 0; i < NG; i++) {
+        int e = -126;
+#pragma unroll
+        for (int k = 0; k < MW; k++)
+          if (meta_group(k) == i) e = max(e, need[k]);
+        e = __reduce_max_sync(kFull, e);
+        if (e > s.E[i]) {
+          e += 1;                                    // a little room, so that this stays rare
+          const float f = p2(s.E[i] - e);
+          set_exponent(s, i, e);
+#pragma unroll
+          for (int j = 0; j < VB; j++)
+            if (j * DB / GS == i)
+#pragma unroll
+              for (int u2 = 0; u2 < MPB; u2++)
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                  for (int k = 0; k < 4; k++) s.acc[j * MPB + u2][t][k] *= f;
+          if ((lane >> 2) == i)
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+              s.bacc[t][0] *= f;
+              s.bacc[t][1] *= f;
+            }
+        }
+      }
+    }
+    __syncwarp();                                    // the buffer's readers of the unit in front are done
+#pragma unroll
+    for (int k = 0; k < MW; k++) {
+      const int i = lane + 32 * k, hg = i / 8, pair = i % 8;
+      const float z = (float)(1 << (BITS - 1)) * s.fb[k];
+      const float s0 = bf_lo(su[k]), s1 = bf_hi(su[k]);
+      if (NG > 1 || lane < 16) {
+        const uint32_t b = pack_h2(fmaf(s0, z, bf_lo(bu[k]) * s.fb[k]), fmaf(s1, z, bf_hi(bu[k]) * s.fb[k]));
+        *reinterpret_cast<uint2 *>(buf + hg * 64 + pair * 8) = make_uint2(b, pack_h2(s0 * s.fs[k], s1 * s.fs[k]));
+      }
+    }
+    __syncwarp();
+  }
+
   // Values of a granule: sum of P * (bias + Z scale) a group, and P * scale against the codes.
-  static __device__ __forceinline__ void values(const unsigned char *sm, const uint32_t (&ph)[NT][2],
-                                                const uint32_t (&pl)[NT][2], State &s) {
+  static __device__ __forceinline__ void values(const unsigned char *sm, const unsigned char *meta,
+                                                const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2], State &s) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG + c * 8, *vb = vs + 32 * NG;
     {
-      // one MMA: row g of A = group g's (lane r < NG)
-      const int g = r % NG;
-      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32), b = *reinterpret_cast<const uint2 *>(vb + g * 32);
-      const float z = (float)(1 << (BITS - 1)) * s.fb;
-      uint32_t a0 = pack_h2(fmaf(bf_lo(u.x), z, bf_lo(b.x) * s.fb), fmaf(bf_hi(u.x), z, bf_hi(b.x) * s.fb));
-      uint32_t a2 = pack_h2(fmaf(bf_lo(u.y), z, bf_lo(b.y) * s.fb), fmaf(bf_hi(u.y), z, bf_hi(b.y) * s.fb));
-      if (NG < 8 && r >= NG) a0 = a2 = 0u;
+      // one MMA: row g of A = group g's (rows of lanes r >= NG repeat them and are not used)
+      const uint4 m = *reinterpret_cast<const uint4 *>(meta + (r % NG) * 64 + c * 16);
 #pragma unroll
       for (int t = 0; t < NT; t++) {
-        mma(s.bacc[t], a0, 0u, a2, 0u, ph[t][0], ph[t][1]);
-        if constexpr (PREC) mma(s.bacc[t], a0, 0u, a2, 0u, pl[t][0], pl[t][1]);
+        mma(s.bacc[t], m.x, m.y, m.z, m.w, ph[t][0], ph[t][1]);
+        if constexpr (PREC) mma(s.bacc[t], m.x, m.y, m.z, m.w, pl[t][0], pl[t][1]);
       }
     }
     // !PREC: subnormal codes, and -Z, -16 Z (4-bit) times 2^-24 for the centring MMA
@@ -435,9 +525,8 @@ struct Kernel {
     uint32_t b[NG][NT][2];
 #pragma unroll
     for (int g = 0; g < NG; g++) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(vs + g * 32);
-      const float f = s.fs[g];
-      const uint32_t s0 = pack_h2(bf_lo(u.x) * f, bf_hi(u.x) * f), s1 = pack_h2(bf_lo(u.y) * f, bf_hi(u.y) * f);
+      const uint4 m = *reinterpret_cast<const uint4 *>(meta + g * 64 + c * 16);
+      const uint32_t s0 = m.y, s1 = m.w;
       uint32_t bl[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; t++) {
@@ -485,9 +574,9 @@ struct Kernel {
   // One unit (two granules): scores, running max, P, values of its tokens lo ..
   // valid - 1, lo 0 or 16 and below valid.  Of the others, scores are masked and
   // value scales and biases must be zero (clear_tail).
-  static __device__ __forceinline__ void unit(const unsigned char *sm, int lo, int valid, const uint32_t (&qf)[KM][NT][2],
+  static __device__ __forceinline__ void unit(const unsigned char *sm, unsigned char *meta, int lo, int valid, const uint32_t (&qf)[KM][NT][2],
                                               const float (&qsum)[NG][NT][2], const float (&sf)[NT][2], State &s) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int lane = threadIdx.x & 31, r = lane >> 2;
     const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8: t0, t0 + 2
     float sc[2][NT][4], y[2][NT][4];
     scores(sm, qf, qsum, sc);
@@ -563,51 +652,9 @@ struct Kernel {
           ph[h][t][k] = transpose8x8(u);
         }
       }
-    // ---- the groups' powers of two: lane r checks group r % NG
-    {
-      const int g = r % NG;
-      const unsigned char *vs = sm + 2 * L.code_bytes + 64 * NG + c * 8 + g * 32;
-      uint32_t su = 0, bu = 0;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-          const uint2 u = *reinterpret_cast<const uint2 *>(vs + h * GB);
-          const uint2 b = *reinterpret_cast<const uint2 *>(vs + h * GB + 32 * NG);
-          su = max_u16x2(su, max_u16x2(u.x, u.y));
-          bu = max_u16x2(bu, max_u16x2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu));
-        }
-      su &= 0x7fff7fffu;
-      const uint32_t s1 = max(su & 0xffffu, su >> 16), b1 = max(bu & 0xffffu, bu >> 16);
-      if (__any_sync(kFull, (s1 > s.lim_s) | (b1 > s.lim_b))) {
-        // exponents that hold scale * 2^BITS and |bias| below 2^E
-        const int need = min(120, max((int)(s1 >> 7) - 126 + BITS, (int)(b1 >> 7) - 126));
-#pragma unroll
-        for (int i = 0; i < NG; i++) {
-          int e = __reduce_max_sync(kFull, g == i ? need : -126);
-          if (e > s.E[i]) {
-            e += 1;                                  // a little room, so that this stays rare
-            const float f = p2(s.E[i] - e);
-            set_exponent(s, i, e, g == i);
-#pragma unroll
-            for (int j = 0; j < VB; j++)
-              if (j * DB / GS == i)
-#pragma unroll
-                for (int u2 = 0; u2 < MPB; u2++)
-#pragma unroll
-                  for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++) s.acc[j * MPB + u2][t][k] *= f;
-            if (r == i)
-#pragma unroll
-              for (int t = 0; t < NT; t++) {
-                s.bacc[t][0] *= f;
-                s.bacc[t][1] *= f;
-              }
-          }
-        }
-      }
-    }
-    values(sm, ph[0], pl[0], s);
-    values(sm + GB, ph[1], pl[1], s);
+    convert_meta(sm, meta, s);
+    values(sm, meta, ph[0], pl[0], s);
+    values(sm + GB, meta + 64 * NG, ph[1], pl[1], s);
   }
 
   // Writes this warp's sums (value units, over 2^kLogP) and max / total to the join buffer.
@@ -679,7 +726,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   float *join = reinterpret_cast<float *>(smem_raw);                         // [warp][GHP][SROW], then [warp][GHP][2]
   float *join_ml = join + kWarps * K::GHP * K::SROW;
-  unsigned char *ring = smem_raw + ((K::kJoin + 15) & ~15) + warp * a.depth * 2 * K::GB;
+  unsigned char *meta = smem_raw + K::kJoin + warp * K::kMeta;
+  unsigned char *ring = smem_raw + K::kJoin + kWarps * K::kMeta + warp * a.depth * 2 * K::GB;
   uint64_t *bar = bars + warp * 8;
 
   if (lane == 0)
@@ -719,29 +767,36 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   const int64_t page_bytes = ((int64_t)a.H << a.gshift) * K::GB;
   auto issue = [&]() {                // the cursor's unit into slot_in
     if (cp.g >= cp.end) return;
-    // the granules to copy: the second only where a token of it is in front of the length (its page may not
-    // exist), neither where its page id is outside the cache (left out and reported)
+    // the second granule only where a token of it is in front of the length (its page may not exist)
     const bool two = cp.g * kUnit + kv::kTok < cp.len;
-    const bool ok0 = (uint32_t)cp.page0 < (uint32_t)a.pages, ok1 = two && (uint32_t)cp.page1 < (uint32_t)a.pages;
-    if (lane == 0) {
-      unsigned char *dst = ring + slot_in * 2 * K::GB;
-      const unsigned char *src = cp.head + cp.page0 * page_bytes + (cp.g * 2 & ((1 << a.gshift) - 1)) * K::GB;
-      if (a.gshift != 0) {                       // both in one page
-        if (ok0) {
-          mbar_arrive_expect_tx(bar + slot_in, two ? 2 * K::GB : K::GB);
-          bulk_load(dst, src, two ? 2 * K::GB : K::GB, bar + slot_in);
-        }
-      } else if (ok0 || ok1) {
-        mbar_arrive_expect_tx(bar + slot_in, ok0 && ok1 ? 2 * K::GB : K::GB);
-        if (ok0) bulk_load(dst, src, K::GB, bar + slot_in);
-        if (ok1) bulk_load(dst + K::GB, cp.head + cp.page1 * page_bytes, K::GB, bar + slot_in);
-      }
-      if (!ok0 || (two && !ok1)) atomicOr(&g_device_error, kErrIndex);
-    }
+    unsigned char *dst = ring + slot_in * 2 * K::GB;
+    uint64_t *full = bar + slot_in;
     const uint32_t bit = 1u << slot_in;
-    filled = ok0 || ok1 ? filled | bit : filled & ~bit;
-    lack0 = ok0 ? lack0 & ~bit : lack0 | bit;
-    lack1 = ok1 ? lack1 & ~bit : lack1 | bit;
+    if (max((uint32_t)cp.page0, (uint32_t)cp.page1) < (uint32_t)a.pages) {
+      if (lane == 0) {
+        const unsigned char *src = cp.head + cp.page0 * page_bytes + (cp.g * 2 & ((1 << a.gshift) - 1)) * K::GB;
+        const uint32_t bytes = two ? 2 * K::GB : K::GB;
+        mbar_arrive_expect_tx(full, bytes);
+        if (a.gshift != 0) {                     // both in one page
+          bulk_load(dst, src, bytes, full);
+        } else {
+          bulk_load(dst, src, K::GB, full);
+          if (two) bulk_load(dst + K::GB, cp.head + cp.page1 * page_bytes, K::GB, full);
+        }
+      }
+      filled |= bit;
+    } else {                                     // a granule whose page is outside the cache is left out and reported
+      const bool ok0 = (uint32_t)cp.page0 < (uint32_t)a.pages, ok1 = two && (uint32_t)cp.page1 < (uint32_t)a.pages;
+      if (lane == 0) {
+        atomicOr(&g_device_error, kErrIndex);
+        if (ok0 || ok1) mbar_arrive_expect_tx(full, K::GB);
+        if (ok0) bulk_load(dst, cp.head + cp.page0 * page_bytes, K::GB, full);      // (gshift 0: else both are bad)
+        if (ok1) bulk_load(dst + K::GB, cp.head + cp.page1 * page_bytes, K::GB, full);
+      }
+      if (ok0 || ok1) filled |= bit;
+      if (!ok0) lack0 |= bit;
+      if (!ok1) lack1 |= bit;
+    }
     slot_in = slot_in + 1 == a.depth ? 0 : slot_in + 1;
     cp.g += kWarps;
     cursor_page(a, cp);
@@ -836,13 +891,15 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
         if (mbar_wait(bar + slot_out, phase >> slot_out & 1u)) {
           unsigned char *sm = ring + slot_out * 2 * K::GB;
           int lo = 0, valid = pc.len - g * kUnit;
-          if (lack0 >> slot_out & 1u) lo = kv::kTok;
-          if (lack1 >> slot_out & 1u) valid = min(valid, kv::kTok);
+          if ((lack0 | lack1) >> slot_out & 1u) {
+            if (lack0 >> slot_out & 1u) lo = kv::kTok;
+            if (lack1 >> slot_out & 1u) valid = min(valid, kv::kTok);
+          }
           if (lo > 0 || valid < kUnit) {
             K::clear_tail(sm, lo > 0 ? 0 : valid);
             K::clear_tail(sm + K::GB, valid - kv::kTok);
           }
-          K::unit(sm, lo, valid, qf, qsum, sf, s);
+          K::unit(sm, meta, lo, valid, qf, qsum, sf, s);
           phase ^= 1u << slot_out;
           filled &= ~(1u << slot_out);
         } else {
@@ -850,6 +907,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
         }
       }
       __syncwarp();
+      lack0 &= ~(1u << slot_out);
+      lack1 &= ~(1u << slot_out);
       slot_out = slot_out + 1 == a.depth ? 0 : slot_out + 1;
       if (!dead) issue();
     }
@@ -1023,7 +1082,7 @@ template <int BITS, int D, int GS, int NT, bool PREC>
 gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   using K = attn::Kernel<BITS, D, GS, NT, PREC>;
   auto kern = attn::k_attn_decode<BITS, D, GS, NT, PREC>;
-  const size_t join = (K::kJoin + 15) & ~15;
+  constexpr size_t join = K::kJoin + attn::kWarps * K::kMeta;   // (both multiples of 16)
   // ring depth: what lets four CTAs share an SM (227 KB less 1 KB a CTA), at least 2 slots, at most 6
   constexpr size_t slot = (size_t)attn::kWarps * 2 * K::GB;
   int depth = join + 1536 < 227 * 1024 / 4 ? (int)((227 * 1024 / 4 - 1536 - join) / slot) : 0;
