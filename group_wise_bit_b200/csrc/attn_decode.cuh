@@ -151,7 +151,7 @@ __device__ __forceinline__ float q_at(const uint16_t *p, int f16) {
 // stay level with shares of long ones.  A share that begins inside a pair's first
 // kPieceCost places begins at its unit 0; one that ends there leaves the pair
 // to the next share.
-constexpr int kPieceCost = 4;
+constexpr int kPieceCost = 16;
 constexpr int kUnit = 2 * kv::kTok;   // tokens of a unit
 
 // Where the share of a CTA begins, and its length.
@@ -231,7 +231,7 @@ __device__ __forceinline__ void cursor_page(const Args &a, Cursor &c) {
   }
 }
 // Opens the piece at place u of (b, hc), skipping empty sequences; false when the share ends in front of it.
-template <int GB>
+template <int GB, bool PAGES = true>
 __device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int first) {
   c.g = c.end = 0;
   while (c.left > 0 && c.b < a.B) {
@@ -247,7 +247,7 @@ __device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int
       c.g = g + first;
       c.head = a.cache + (((int64_t)(c.hc / a.chunks)) << a.gshift) * GB;
       c.row = a.table + (int64_t)c.b * a.table_stride;
-      cursor_page(a, c);
+      if constexpr (PAGES) cursor_page(a, c);
       return true;
     }
     c.b++;
@@ -256,13 +256,13 @@ __device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int
   c.left = 0;
   return false;
 }
-template <int GB>
+template <int GB, bool PAGES = true>
 __device__ __forceinline__ bool cursor_next_piece(const Args &a, Cursor &c, int first) {
   if (++c.hc == a.H * a.chunks) {
     c.hc = 0;
     c.b++;
   }
-  return cursor_open<GB>(a, c, 0, first);
+  return cursor_open<GB, PAGES>(a, c, 0, first);
 }
 // Leaves a warp's cursor on a granule of its own, or at the end (g >= end, left == 0).
 template <int GB>
@@ -272,7 +272,7 @@ __device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int firs
 
 // Resident CTAs an SM that the registers are held to: 16 warps where 128
 // registers a thread hold the state, 8 where it takes more.
-constexpr int min_ctas(int D, int NT) { return D * NT <= 128 ? 4 : 2; }
+constexpr int min_ctas(int D, int NT) { return D * NT <= 128 ? 3 : 2; }
 
 template <int BITS, int D, int GS, int NT, bool PREC>
 struct Kernel {
@@ -300,6 +300,7 @@ struct Kernel {
     uint32_t lim_s[MW], lim_b[MW];   // and the largest scale and |bias| (bf16 bits, in both halves) that 2^E holds
   };
   static constexpr int kMeta = 128 * NG;              // bytes of a warp's converted scales and biases
+  static constexpr int kQ = GHP * D * 2;              // bytes of a piece's queries
   static __device__ __forceinline__ int meta_group(int k) { return (((threadIdx.x & 31) + 32 * k) / 8) % NG; }
 
   static __device__ __forceinline__ void set_exponent(State &s, int g, int e) {
@@ -727,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   float *join = reinterpret_cast<float *>(smem_raw);                         // [warp][GHP][SROW], then [warp][GHP][2]
   float *join_ml = join + kWarps * K::GHP * K::SROW;
   unsigned char *meta = smem_raw + K::kJoin + warp * K::kMeta;
-  unsigned char *ring = smem_raw + K::kJoin + kWarps * K::kMeta + warp * a.depth * 2 * K::GB;
+  unsigned char *qbuf = smem_raw + K::kJoin + kWarps * K::kMeta;             // queries of a piece
+  unsigned char *ring = qbuf + K::kQ + warp * a.depth * 2 * K::GB;
   uint64_t *bar = bars + warp * 8;
 
   if (lane == 0)
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   cp.b = pc.b = start.b;
   cp.hc = pc.hc = start.hc;
   cp.left = pc.left = start.left;
-  if (!cursor_open<K::GB>(a, pc, start.u, 0)) {
+  if (!cursor_open<K::GB, false>(a, pc, start.u, 0)) {
     if (tid == 0) recs[blockIdx.x] = Rec{0, 0, 0, 0};
     return;
   }
@@ -802,34 +804,44 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     cursor_page(a, cp);
     cursor_settle<K::GB>(a, cp, warp);
   };
+  // queries of a piece into their buffer: heads [h0, h0 + heads) of the kv head's chunk
+  auto fetch_q = [&](const Cursor &c) {
+    const int chunk = c.hc % a.chunks;
+    const int n = min(a.GH, a.G - chunk * a.GH) * (D / 8);
+    const uint16_t *src = a.q + (int64_t)c.b * a.q_stride + (int64_t)((c.hc / a.chunks) * a.G + chunk * a.GH) * D;
+    for (int i = tid; i < n; i += kThreads) cp_async_16(qbuf + i * 16, src + i * 8, 16);
+    cp_async_commit();
+  };
+  fetch_q(pc);
   for (int i = 0; i < a.depth; i++) issue();
 
   typename K::State s;
   int g_first = pc.g;
   bool first_piece = true;
   while (true) {
+    cp_async_wait<0>();
+    __syncthreads();                  // this piece's queries are there, and the join buffer is free
     // ---- this piece's queries: chunk of heads [h0, h0 + heads) of kv head pc.hc / chunks
     const int chunk = pc.hc % a.chunks;
     const int h0 = (pc.hc / a.chunks) * a.G + chunk * a.GH;
     const int heads = min(a.GH, a.G - chunk * a.GH);
     uint32_t qf[K::KM][NT][2];
     float qsum[K::NG][NT][2], sf[NT][2];
-    const uint16_t *q = a.q + (int64_t)pc.b * a.q_stride;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       // lane r holds head 8t + r; its elements in the order of the score MMAs
       const bool in = 8 * t + r < heads;
-      const uint16_t *row = q + (int64_t)(h0 + (in ? 8 * t + r : 0)) * D;
+      const unsigned char *row = qbuf + (in ? 8 * t + r : 0) * (2 * D);
       float v[D / 4], mx = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 32; i++) {
         // 4-bit: word 4i + c covers elements 32i + 8c ..+7; 8-bit: words 8i + c and 8i + 4 + c, four each
         uint32_t p[4];
         if constexpr (BITS == 4) {
-          *reinterpret_cast<uint4 *>(p) = __ldg(reinterpret_cast<const uint4 *>(row + 32 * i + 8 * c));
+          *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(row + 64 * i + 16 * c);
         } else {
-          *reinterpret_cast<uint2 *>(p) = __ldg(reinterpret_cast<const uint2 *>(row + 32 * i + 4 * c));
-          *reinterpret_cast<uint2 *>(p + 2) = __ldg(reinterpret_cast<const uint2 *>(row + 32 * i + 16 + 4 * c));
+          *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(row + 64 * i + 8 * c);
+          *reinterpret_cast<uint2 *>(p + 2) = *reinterpret_cast<const uint2 *>(row + 64 * i + 32 + 8 * c);
         }
 #pragma unroll
         for (int e = 0; e < 8; e++) {
@@ -884,6 +896,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
       }
     }
     K::reset(s);
+    Cursor nc = pc;
+    const bool more = cursor_next_piece<K::GB, false>(a, nc, 0);
+    __syncthreads();                  // every warp holds its queries
+    if (more) fetch_q(nc);            // (in flight through the piece's loop)
 
     // ---- this warp's units of the piece
     for (int g = g_first + warp; g < pc.end; g += kWarps) {
@@ -953,10 +969,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
         }
       }
     }
-    if (!cursor_next_piece<K::GB>(a, pc, 0)) break;
+    if (!more) break;
+    pc = nc;
     first_piece = false;
     g_first = 0;
-    __syncthreads();
   }
   // copies still in flight (only after a wait gave up) land before the CTA's memory is freed
   if (dead)
@@ -964,18 +980,21 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
       if (filled >> i & 1u) mbar_wait(bar + i, phase >> i & 1u);
 }
 
-// Joins the pieces of a pair that shares cut.  Blocks (i, h) look at the
-// boundary in front of share i: if it is the first one inside its pair, block h
-// adds head h of the piece that ends share i - 1 and of those that begin share
-// i, i + 1, ...: the warps take pieces in turn, a lane D / 32 elements.
+// Joins the pieces of a pair that shares cut.  Block i looks at the boundary in
+// front of share i: if it is the first one inside its pair, the block adds the
+// piece that ends share i - 1 and those that begin share i, i + 1, ...: kJoinWarps
+// warps share the heads and, where they are more, a head's pieces; a lane takes
+// D / 32 elements.
+constexpr int kJoinWarps = 16;
+
 template <int D, int GHP>
-__global__ void __launch_bounds__(kThreads) k_attn_join(const Args a, int ctas) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const Args a, int ctas) {
   constexpr int kPart = Ws<D, GHP>::kPart, E = D / 32;
-  __shared__ float so[kWarps][D], sml[kWarps][2];
+  __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
   pdl_launch_dependents();
   pdl_wait();
   const Rec *recs = reinterpret_cast<const Rec *>(a.ws + (int64_t)2 * ctas * kPart);
-  const int i = blockIdx.x + 1, h = blockIdx.y;
+  const int i = blockIdx.x + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (read through L2: nothing of the workspace may come from an earlier launch's lines in L1)
   auto rec_at = [&](int j) {
@@ -987,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const Args a, int ctas) 
   if (prev.b == rec.b && prev.hc == rec.hc && prev.g0 > 0) return;   // an earlier boundary is inside this pair
   const int chunk = rec.hc % a.chunks;
   const int h0 = (rec.hc / a.chunks) * a.G + chunk * a.GH;
-  if (h >= min(a.GH, a.G - chunk * a.GH)) return;
+  const int heads = min(a.GH, a.G - chunk * a.GH);
   int last = i;                                                      // shares that begin inside the pair
   for (bool more = true; more;) {
     const int j = last + 1 + lane;
@@ -1001,51 +1020,69 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const Args a, int ctas) 
   // piece j = 0: end of share i - 1; j > 0: beginning of share i + j - 1
   auto part = [&](int j) { return a.ws + (int64_t)(j == 0 ? 2 * (i - 1) + 1 : 2 * (i + j - 1)) * kPart; };
   const int pieces = last - i + 2;
-  float m = -INFINITY, l = 0.0f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; e++) o[e] = 0.0f;
-#pragma unroll 4
-  for (int j = warp; j < pieces; j += kWarps) {
-    const float *p = part(j);
-    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + GHP * D + 2 * h));
-    float v[E];
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 t = __ldcg(reinterpret_cast<const float2 *>(p + h * D + lane * E + e));
-      v[e] = t.x;
-      v[e + 1] = t.y;
+  int per = 1;                                                       // warps of a head
+  while (per * 2 * heads <= kJoinWarps) per *= 2;
+  const int h = warp / per, w = warp % per;
+  if (h < heads) {
+    // the common max first (lanes look at 32 pieces at once), so that the sums' loads do not wait for one another
+    auto ml_at = [&](int j) { return __ldcg(reinterpret_cast<const float2 *>(part(j) + GHP * D + 2 * h)); };
+    float m = -INFINITY, l = 0.0f, o[E];
+    for (int j = w + lane * per; j < pieces; j += 32 * per) {
+      const float2 ml = ml_at(j);
+      if (ml.y != 0.0f) m = fmaxf(m, ml.x);                          // (a piece without a token adds nothing)
     }
-    const float mn = ml.y == 0.0f ? m : fmaxf(m, ml.x);              // (a piece without a token adds nothing)
-    const float fo = m == -INFINITY ? 0.0f : ex2(m - mn), fj = ml.y == 0.0f ? 0.0f : ex2(ml.x - mn);
-    m = mn;
-    l = fmaf(ml.y, fj, l * fo);
 #pragma unroll
-    for (int e = 0; e < E; e++) o[e] = ml.y == 0.0f ? o[e] : fmaf(v[e], fj, o[e] * fo);
-  }
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
 #pragma unroll
-  for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    sml[warp][0] = m;
-    sml[warp][1] = l;
+    for (int e = 0; e < E; e++) o[e] = 0.0f;
+    for (int j0 = w; j0 < pieces; j0 += 32 * per) {
+      float f = 0.0f, lj = 0.0f;                                     // of piece j0 + lane * per
+      if (j0 + lane * per < pieces) {
+        const float2 ml = ml_at(j0 + lane * per);
+        lj = ml.y;
+        f = lj == 0.0f ? 0.0f : ex2(ml.x - m);
+      }
+      l = fmaf(lj, f, l);
+      const int n = min(32, (pieces - j0 + per - 1) / per);
+#pragma unroll 8
+      for (int k = 0; k < n; k++) {
+        const float *p = part(j0 + k * per) + h * D + lane * E;
+        const float fk = __shfl_sync(kFull, f, k);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(p + e));
+          o[e] = fmaf(v.x, fk, o[e]);
+          o[e + 1] = fmaf(v.y, fk, o[e + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
+#pragma unroll
+    for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      sml[warp][0] = m;
+      sml[warp][1] = l;
+    }
   }
   __syncthreads();
-  if (threadIdx.x * 2 >= D) return;
-  float mt = -INFINITY, lt = 0.0f, x0 = 0.0f, x1 = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWarps; w++)
-    if (sml[w][1] != 0.0f) mt = fmaxf(mt, sml[w][0]);
-#pragma unroll
-  for (int w = 0; w < kWarps; w++) {
-    if (sml[w][1] == 0.0f) continue;
-    const float f = ex2(sml[w][0] - mt);
-    lt = fmaf(sml[w][1], f, lt);
-    x0 = fmaf(so[w][2 * threadIdx.x], f, x0);
-    x1 = fmaf(so[w][2 * threadIdx.x + 1], f, x1);
+  for (int x = threadIdx.x; x < heads * (D / 2); x += kJoinWarps * 32) {
+    const int hh = x / (D / 2), d = x % (D / 2) * 2;
+    float mt = -INFINITY, lt = 0.0f, x0 = 0.0f, x1 = 0.0f;
+    for (int k = hh * per; k < (hh + 1) * per; k++)
+      if (sml[k][1] != 0.0f) mt = fmaxf(mt, sml[k][0]);
+    for (int k = hh * per; k < (hh + 1) * per; k++) {
+      if (sml[k][1] == 0.0f) continue;
+      const float f = ex2(sml[k][0] - mt);
+      lt = fmaf(sml[k][1], f, lt);
+      x0 = fmaf(so[k][d], f, x0);
+      x1 = fmaf(so[k][d + 1], f, x1);
+    }
+    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+    const int64_t row = (int64_t)rec.b * a.H * a.G + h0 + hh;
+    store_out2(a, row * D + d, x0 * inv, x1 * inv);
+    if (a.lse && d == 0) a.lse[row] = lse_of(mt, lt);
   }
-  const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-  const int64_t row = (int64_t)rec.b * a.H * a.G + h0 + h;
-  store_out2(a, row * D + 2 * threadIdx.x, x0 * inv, x1 * inv);
-  if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(mt, lt);
 }
 
 }  // namespace attn
@@ -1071,7 +1108,7 @@ attn::Args attn_args(const AttnCall &c) {
   while (gpp >>= 1) a.gshift++;
   const int64_t cap = c.max_pages * c.cache.page_size;
   a.cap = (int)(cap < 0x7fffff00 ? cap : 0x7fffff00);          // (a whole number of units)
-  a.min_per = attn::kPieceCost + attn::kWarps;
+  a.min_per = attn::kWarps;
   a.f16 = c.f16;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   return a;
@@ -1082,10 +1119,11 @@ template <int BITS, int D, int GS, int NT, bool PREC>
 gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   using K = attn::Kernel<BITS, D, GS, NT, PREC>;
   auto kern = attn::k_attn_decode<BITS, D, GS, NT, PREC>;
-  constexpr size_t join = K::kJoin + attn::kWarps * K::kMeta;   // (both multiples of 16)
-  // ring depth: what lets four CTAs share an SM (227 KB less 1 KB a CTA), at least 2 slots, at most 6
-  constexpr size_t slot = (size_t)attn::kWarps * 2 * K::GB;
-  int depth = join + 1536 < 227 * 1024 / 4 ? (int)((227 * 1024 / 4 - 1536 - join) / slot) : 0;
+  constexpr size_t join = K::kJoin + attn::kWarps * K::kMeta + K::kQ;   // (all multiples of 16)
+  // ring depth: what lets the CTAs that the registers allow share an SM (227 KB less 1 KB a CTA and the
+  // kernel's static part), at least 2 slots, at most 6
+  constexpr size_t slot = (size_t)attn::kWarps * 2 * K::GB, most = 227 * 1024 / attn::min_ctas(D, NT) - 1536;
+  int depth = join < most ? (int)((most - join) / slot) : 0;
   depth = depth < 2 ? 2 : (depth > 6 ? 6 : depth);
   const size_t smem = join + depth * slot;
   AttnSetup su;
@@ -1108,7 +1146,8 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
-  cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)a.GH);
+  cfg.gridDim = dim3((unsigned)(ctas - 1));
+  cfg.blockDim = dim3(attn::kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, attn::k_attn_join<D, K::GHP>, a, ctas);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode join launch: %s", cudaGetErrorString(e));
