@@ -375,8 +375,13 @@ def _here(*tensors):
     """All given tensors lie on the current CUDA device (the one whose stream the call goes to)."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _out_like(t, name, like, dtype):
+    """_out for an output of like's shape (less host time than torch.empty)."""
+    return torch.empty_like(like, dtype=dtype) if t is None else _dev(t, name, (dtype,), like.shape)
 
 
 def _token_rows(t, name, shape, dtypes):
@@ -407,10 +412,10 @@ def rmsnorm_quant_i8(x, weight, eps, residual=None, residual_out=None, qx=None, 
     _dev(weight, "weight", dt, (K,))
     if residual is not None:
         _dev(residual, "residual", dt, (M, K))
-        residual_out = _out(residual_out, "residual_out", (M, K), x.dtype, x.device)
+        residual_out = _out_like(residual_out, "residual_out", x, x.dtype)
     elif residual_out is not None:
         raise ValueError("residual_out without residual: the sum would be x itself")
-    qx = _out(qx, "qx", (M, K), torch.int8, x.device)
+    qx = _out_like(qx, "qx", x, torch.int8)
     sx = _out(sx, "sx", (M,), torch.float32, x.device)
     _here(x, weight, residual, residual_out, qx, sx)
     _call("gwb_rmsnorm_quant_i8", _ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _HALF[x.dtype],
@@ -425,7 +430,7 @@ def dequant_per_token_i8(qx, sx, dtype=torch.bfloat16, out=None):
     _dev(sx, "sx", (torch.float32,), (M,))
     if dtype not in _HALF:
         raise TypeError(f"dtype {dtype} not in {tuple(_HALF)}")
-    out = _out(out, "out", (M, K), dtype, qx.device)
+    out = _out_like(out, "out", qx, dtype)
     _here(qx, sx, out)
     _call("gwb_dequant_per_token_i8", _ptr(qx), _ptr(sx), M, K, _HALF[dtype], _ptr(out), _stream())
     return out
@@ -490,7 +495,7 @@ def kv_read(cache, slots, head_dim, bits, group_size, dtype=torch.bfloat16, k=No
     shape = (slots.numel(), heads, head_dim)
     _dev(slots, "slots", (torch.int64,), shape[:1])
     k = _out(k, "k", shape, dtype, cache.device)
-    v = _out(v, "v", shape, dtype, cache.device)
+    v = _out_like(v, "v", k, dtype)
     _here(cache, slots, k, v)
     _call("gwb_kv_read", _ptr(cache), pages, heads, page_size, head_dim, bits, group_size, _ptr(slots), shape[0],
           _HALF[dtype], _ptr(k), _ptr(v), _stream())

@@ -72,6 +72,7 @@ struct Args {
   int depth;                    // ring slots a warp
   int min_per;                  // least places of a share
   int f16;
+  int direct;                   // a CTA a pair: no pair is cut
   float scale_log2;             // softmax scale * log2 e
 };
 
@@ -737,7 +738,18 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   fence_mbar_init();
   pdl_launch_dependents();
   pdl_wait();
-  find_start(a, &start, scan);   // (its barriers also publish the mbarriers)
+  if (a.direct) {
+    if (tid == 0) {
+      const int HC = a.H * a.chunks;
+      start.b = blockIdx.x / HC;
+      start.hc = blockIdx.x % HC;
+      start.u = 0;
+      start.left = places(units(tokens(a, start.b, start.hc == 0)));
+    }
+    __syncthreads();
+  } else {
+    find_start(a, &start, scan);
+  }                              // (the barriers also publish the mbarriers)
 
   // rows without a token: zeros, and minus infinity for the log-sum-exp
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)
@@ -755,12 +767,12 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   cp.hc = pc.hc = start.hc;
   cp.left = pc.left = start.left;
   if (!cursor_open<K::GB, false>(a, pc, start.u, 0)) {
-    if (tid == 0) recs[blockIdx.x] = Rec{0, 0, 0, 0};
+    if (tid == 0 && !a.direct) recs[blockIdx.x] = Rec{0, 0, 0, 0};
     return;
   }
   cursor_open<K::GB>(a, cp, start.u, warp);
   cursor_settle<K::GB>(a, cp, warp);
-  if (tid == 0) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
+  if (tid == 0 && !a.direct) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
 
   uint32_t filled = 0, phase = 0;     // slots with a copy, parity of each slot's next wait
   uint32_t lack0 = 0, lack1 = 0;      // slots without their first / second granule
@@ -1114,6 +1126,15 @@ attn::Args attn_args(const AttnCall &c) {
   return a;
 }
 
+// A CTA a pair, without cuts and without a join, where every sequence is short, or where the pairs are many
+// and none is long enough to keep one CTA busy behind the others.  us, direct against cut (4 bits, head_dim
+// 128, 8 kv heads, tables of L tokens, lengths L/2 .. L): 1 sequence of 128 tokens 5.1 / 7.3, of 512 8.7 / 10.2,
+// of 1024 13.7 / 10.8; 64 sequences of 512 19.1 / 23.0, of 2048 46.4 / 43.9; 256 of 512 50.2 / 57.3, of 2048
+// 125 / 142.
+inline bool attn_direct(int64_t pairs, int64_t cap, int ctas) {
+  return pairs <= 65536 && (cap <= 512 || (cap <= 2048 && pairs >= 4 * (int64_t)ctas));
+}
+
 // Launches of one instance: the attention, then the join that depends on it.
 template <int BITS, int D, int GS, int NT, bool PREC>
 gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
@@ -1134,8 +1155,10 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   if (ws_bytes < need)
     return fail(GWB_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
   a.depth = depth;
+  const int64_t pairs = (int64_t)a.B * a.H * a.chunks;
+  a.direct = attn_direct(pairs, a.cap, ctas);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3(a.direct ? (unsigned)pairs : (unsigned)ctas);
   cfg.blockDim = dim3(attn::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -1146,6 +1169,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
+  if (a.direct) return GWB_OK;
   cfg.gridDim = dim3((unsigned)(ctas - 1));
   cfg.blockDim = dim3(attn::kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
