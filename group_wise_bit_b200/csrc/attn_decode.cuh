@@ -72,9 +72,12 @@ struct Args {
   int depth;                    // ring slots a warp
   int min_per;                  // least places of a share
   int f16;
-  int direct;                   // a CTA a pair: no pair is cut
+  int mode;                     // kCut, kCtaPair, kWarpPair
   float scale_log2;             // softmax scale * log2 e
 };
+
+// How pairs are spread: cut into equal shares; a CTA a pair; a warp a pair (no pair is cut in the last two).
+enum { kCut = 0, kCtaPair = 1, kWarpPair = 2 };
 
 // One record a CTA: the first piece of its share.
 struct Rec {
@@ -729,8 +732,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   float *join = reinterpret_cast<float *>(smem_raw);                         // [warp][GHP][SROW], then [warp][GHP][2]
   float *join_ml = join + kWarps * K::GHP * K::SROW;
   unsigned char *meta = smem_raw + K::kJoin + warp * K::kMeta;
-  unsigned char *qbuf = smem_raw + K::kJoin + kWarps * K::kMeta;             // queries of a piece
-  unsigned char *ring = qbuf + K::kQ + warp * a.depth * 2 * K::GB;
+  unsigned char *qcta = smem_raw + K::kJoin + kWarps * K::kMeta;             // queries of a piece
+  unsigned char *ring = qcta + K::kQ + warp * a.depth * 2 * K::GB;
   uint64_t *bar = bars + warp * 8;
 
   if (lane == 0)
@@ -738,17 +741,23 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   fence_mbar_init();
   pdl_launch_dependents();
   pdl_wait();
-  if (a.direct) {
-    if (tid == 0) {
-      const int HC = a.H * a.chunks;
-      start.b = blockIdx.x / HC;
-      start.hc = blockIdx.x % HC;
-      start.u = 0;
-      start.left = places(units(tokens(a, start.b, start.hc == 0)));
-    }
-    __syncthreads();
-  } else {
+  // warps that share a pair, this one's number among them, and their barrier
+  const bool alone = a.mode == kWarpPair;
+  const int ways = alone ? 1 : kWarps, way = alone ? 0 : warp;
+  auto pair_sync = [&]() {
+    if (alone) __syncwarp();
+    else __syncthreads();
+  };
+  Start st{};
+  if (a.mode == kCut) {
     find_start(a, &start, scan);
+    st = start;
+  } else {
+    const int HC = a.H * a.chunks, pair = alone ? blockIdx.x * kWarps + warp : blockIdx.x;
+    st.b = pair / HC;
+    st.hc = pair % HC;
+    if (st.b < a.B) st.left = places(units(tokens(a, st.b, st.hc == 0)));
+    pair_sync();
   }                              // (the barriers also publish the mbarriers)
 
   // rows without a token: zeros, and minus infinity for the log-sum-exp
@@ -763,16 +772,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   Rec *recs = reinterpret_cast<Rec *>(a.ws + (int64_t)2 * gridDim.x * kPart);
   // pieces walked by the whole CTA (pc), and this warp's copies (cp), ahead of it
   Cursor cp{}, pc{};
-  cp.b = pc.b = start.b;
-  cp.hc = pc.hc = start.hc;
-  cp.left = pc.left = start.left;
-  if (!cursor_open<K::GB, false>(a, pc, start.u, 0)) {
-    if (tid == 0 && !a.direct) recs[blockIdx.x] = Rec{0, 0, 0, 0};
+  cp.b = pc.b = st.b;
+  cp.hc = pc.hc = st.hc;
+  cp.left = pc.left = st.left;
+  if (!cursor_open<K::GB, false>(a, pc, st.u, 0)) {
+    if (tid == 0 && a.mode == kCut) recs[blockIdx.x] = Rec{0, 0, 0, 0};
     return;
   }
-  cursor_open<K::GB>(a, cp, start.u, warp);
-  cursor_settle<K::GB>(a, cp, warp);
-  if (tid == 0 && !a.direct) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
+  cursor_open<K::GB>(a, cp, st.u, way);
+  cursor_settle<K::GB>(a, cp, way);
+  if (tid == 0 && a.mode == kCut) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
 
   uint32_t filled = 0, phase = 0;     // slots with a copy, parity of each slot's next wait
   uint32_t lack0 = 0, lack1 = 0;      // slots without their first / second granule
@@ -812,16 +821,18 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
       if (!ok1) lack1 |= bit;
     }
     slot_in = slot_in + 1 == a.depth ? 0 : slot_in + 1;
-    cp.g += kWarps;
+    cp.g += ways;
     cursor_page(a, cp);
-    cursor_settle<K::GB>(a, cp, warp);
+    cursor_settle<K::GB>(a, cp, way);
   };
+  // (a warp alone keeps its queries in its part of the join buffer, which it writes after it has read them)
+  unsigned char *qbuf = alone ? reinterpret_cast<unsigned char *>(join + warp * K::GHP * K::SROW) : qcta;
   // queries of a piece into their buffer: heads [h0, h0 + heads) of the kv head's chunk
   auto fetch_q = [&](const Cursor &c) {
     const int chunk = c.hc % a.chunks;
     const int n = min(a.GH, a.G - chunk * a.GH) * (D / 8);
     const uint16_t *src = a.q + (int64_t)c.b * a.q_stride + (int64_t)((c.hc / a.chunks) * a.G + chunk * a.GH) * D;
-    for (int i = tid; i < n; i += kThreads) cp_async_16(qbuf + i * 16, src + i * 8, 16);
+    for (int i = alone ? lane : tid; i < n; i += 32 * ways) cp_async_16(qbuf + i * 16, src + i * 8, 16);
     cp_async_commit();
   };
   fetch_q(pc);
@@ -832,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   bool first_piece = true;
   while (true) {
     cp_async_wait<0>();
-    __syncthreads();                  // this piece's queries are there, and the join buffer is free
+    pair_sync();                      // this piece's queries are there, and the join buffer is free
     // ---- this piece's queries: chunk of heads [h0, h0 + heads) of kv head pc.hc / chunks
     const int chunk = pc.hc % a.chunks;
     const int h0 = (pc.hc / a.chunks) * a.G + chunk * a.GH;
@@ -910,11 +921,11 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     K::reset(s);
     Cursor nc = pc;
     const bool more = cursor_next_piece<K::GB, false>(a, nc, 0);
-    __syncthreads();                  // every warp holds its queries
+    pair_sync();                      // every warp holds its queries
     if (more) fetch_q(nc);            // (in flight through the piece's loop)
 
     // ---- this warp's units of the piece
-    for (int g = g_first + warp; g < pc.end; g += kWarps) {
+    for (int g = g_first + way; g < pc.end; g += ways) {
       if ((filled >> slot_out & 1u) && !dead) {
         if (mbar_wait(bar + slot_out, phase >> slot_out & 1u)) {
           unsigned char *sm = ring + slot_out * 2 * K::GB;
@@ -943,6 +954,19 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
 
     // ---- join the warps: row h of every warp's sums, scaled to the common max
     K::to_join(s, join + warp * K::GHP * K::SROW, join_ml + warp * K::GHP * 2);
+    if (alone) {
+      __syncwarp();
+      for (int i = lane; i < heads * (D / 4); i += 32) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        const float l = join_ml[(warp * K::GHP + h) * 2 + 1], inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float4 o = *reinterpret_cast<const float4 *>(join + (warp * K::GHP + h) * K::SROW + d);
+        const int64_t row = (int64_t)pc.b * a.H * a.G + h0 + h;
+        store_out2(a, row * D + d, o.x * inv, o.y * inv);
+        store_out2(a, row * D + d + 2, o.z * inv, o.w * inv);
+        if (a.lse && d == 0) a.lse[row] = lse_of(join_ml[(warp * K::GHP + h) * 2], l);
+      }
+      break;
+    }
     __syncthreads();
     const bool whole = g_first == 0 && pc.end == pc.n;
     const int64_t part_id = (int64_t)blockIdx.x * 2 + (first_piece && g_first > 0 ? 0 : 1);
@@ -1126,13 +1150,19 @@ attn::Args attn_args(const AttnCall &c) {
   return a;
 }
 
-// A CTA a pair, without cuts and without a join, where every sequence is short, or where the pairs are many
-// and none is long enough to keep one CTA busy behind the others.  us, direct against cut (4 bits, head_dim
-// 128, 8 kv heads, tables of L tokens, lengths L/2 .. L): 1 sequence of 128 tokens 5.1 / 7.3, of 512 8.7 / 10.2,
-// of 1024 13.7 / 10.8; 64 sequences of 512 19.1 / 23.0, of 2048 46.4 / 43.9; 256 of 512 50.2 / 57.3, of 2048
-// 125 / 142.
-inline bool attn_direct(int64_t pairs, int64_t cap, int ctas) {
-  return pairs <= 65536 && (cap <= 512 || (cap <= 2048 && pairs >= 4 * (int64_t)ctas));
+// Short sequences are not cut (one launch, nothing to join): a pair goes to a CTA, or to a warp where the pairs
+// are so many that the SMs want more of them at once.  us for B sequences of tables of L tokens (lengths L/2 .. L,
+// 4 bits, head_dim 128, 8 kv heads; 444 CTAs resident), cut / a CTA a pair / a warp a pair:
+//   B = 1    L = 128    7.3   5.0   8.6     512   10.6   8.9  22.6     1024   10.9  13.8
+//   B = 64   L = 128   15.5  11.6  11.5     512   22.9  19.0  28.7     1024   29.3  27.7     2048   44.5  47.4
+//   B = 128  L = 256   24.8  21.8  19.4     512   31.5  28.5  32.2     2048   74.7  75.1
+//   B = 256  L = 128   30.1  28.4  19.3     512   58.8  51.0  45.0     1024   85.9  77.2  81.2     2048  142  127
+// A longer table may hold one sequence that keeps its CTA busy behind all others, so it is always cut.
+inline int attn_mode(int64_t pairs, int64_t cap, int ctas) {
+  if (pairs > 1 << 20) return attn::kCut;
+  if (cap <= 512 && cap * ctas <= 128 * pairs) return attn::kWarpPair;
+  if (cap <= 512 || (cap <= 2048 && pairs >= 4 * (int64_t)ctas)) return attn::kCtaPair;
+  return attn::kCut;
 }
 
 // Launches of one instance: the attention, then the join that depends on it.
@@ -1156,9 +1186,9 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
     return fail(GWB_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
   a.depth = depth;
   const int64_t pairs = (int64_t)a.B * a.H * a.chunks;
-  a.direct = attn_direct(pairs, a.cap, ctas);
+  a.mode = attn_mode(pairs, a.cap, ctas);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.direct ? (unsigned)pairs : (unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)(a.mode == attn::kCut ? ctas : a.mode == attn::kCtaPair ? pairs : (pairs + attn::kWarps - 1) / attn::kWarps));
   cfg.blockDim = dim3(attn::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -1169,7 +1199,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
-  if (a.direct) return GWB_OK;
+  if (a.mode != attn::kCut) return GWB_OK;
   cfg.gridDim = dim3((unsigned)(ctas - 1));
   cfg.blockDim = dim3(attn::kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;

@@ -357,6 +357,32 @@ def test_attention_long_ragged_and_wide_batches(H, lens):
     Batch(lens[:40], H, 2, 64, 8, 32, 16, "fp16", seed=len(lens)).check()
 
 
+@pytest.mark.parametrize("B,H,G,D,bits,gs,page,most", [
+    (3, 2, 4, 128, 4, 64, 16, 512),        # a CTA a pair
+    (1, 1, 1, 64, 8, 32, 512, 512),        # one pair
+    (150, 8, 2, 64, 4, 32, 16, 96),        # a warp a pair, a last CTA with idle warps
+    (37, 16, 20, 128, 8, 64, 32, 128),     # the same with three chunks of heads
+    (90, 7, 9, 256, 4, 128, 64, 64),
+    (230, 8, 1, 64, 4, 64, 128, 1500),     # a CTA a pair, many pairs of middling length
+])
+def test_attention_uncut_pairs(B, H, G, D, bits, gs, page, most):
+    """Short tables go a pair a CTA or a pair a warp; rows are empty, of one token, full and between."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, most + 1, B)
+    lens[: min(B, 3)] = [most, 0, 1][: min(B, 3)]
+    if B > 100:
+        lens[rng.permutation(B)[: B // 2]] %= 40      # (keeps the oracle quick)
+    b = Batch(lens, H, G, D, bits, gs, page, "bf16", seed=B)
+    first = b.run()
+    b.check(first)
+    again = b.run()
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    b.lens[:] = 0                                      # nothing but empty rows
+    b.args[3].zero_()
+    b.check()
+    gwb.check_device_error()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("kw", [dict(q_spread=30.0), dict(k_spread=20.0), dict(v_spread=1e-3), dict(v_spread=300.0),
                                 dict(v_shift=50.0), dict(k_spread=0.0, v_spread=0.0), dict(q_spread=0.0)],
