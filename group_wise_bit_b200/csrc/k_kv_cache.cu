@@ -1,11 +1,16 @@
 // Writing tokens' keys and values into the paged, quantized cache, and reading
 // rows of it back.
 //
-// Eight consecutive elements of a row (16 bytes of bf16 or fp16) belong to one
-// lane; D / 8 lanes hold a row of one (token, head, key or value), and the
-// gs / 8 lanes of a group find its min and max with shuffles.  The arithmetic is
-// qpack_affine's (fp32, one IEEE rounding a step, bf16 scale and bias), so codes,
-// scales and biases are bit-exact.
+// A block takes 16 tokens, keys or values, and some heads in turn: 16 consecutive
+// elements of a row (32 bytes of bf16 or fp16) belong to one thread, D / 16
+// threads hold a row, and a thread's token, slot and place in the granule stay the
+// same from head to head.  The arithmetic is qpack_affine's (fp32, one IEEE
+// rounding a step, bf16 scale and bias): the gs / 16 threads of a group find its
+// min and max with shuffles, and codes, scales and biases are bit-exact.
+//
+// Where a block's 16 slots are one granule, as in a prompt, its codes and metadata
+// go through shared memory in the cache's order and move in 16-byte pieces; else
+// every thread moves its own 2- and 4-byte units.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,14 +23,14 @@ namespace gwb {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 256;
+constexpr int kE = 16;                    // elements of a thread
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &u, float *v) {
   const uint32_t p[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -46,61 +51,86 @@ struct KvArgs {
   int64_t k_stride, v_stride;
   const int64_t *slots;
   unsigned char *cache;
-  int64_t total_slots;
-  uint32_t rows;               // T * H
+  int64_t T, total_slots;
   int H, page_shift;
+  int heads;                   // of a block
 };
 
-// This lane's place: row (token, head) and element 8 * l in it; blockIdx.y: keys or values.
+// A thread's place: token t, element kE * l of a row, heads
+// [h0, h1); blockIdx.y: keys or values.
 struct Place {
-  uint32_t row, t;
-  int h, l;
+  int64_t t, gran;             // token; granule of its slot in head 0
+  int l, h0, h1, tok;          // tok: place in the granule
+  bool live, whole;            // the slot is in the cache; the block's slots are one granule
 };
 template <int D>
 __device__ __forceinline__ Place place_of(const KvArgs &a) {
-  constexpr int LR = D / 8;
+  constexpr int LR = D / kE;
   Place p;
-  p.row = blockIdx.x * (kThreads / LR) + threadIdx.x / LR;
+  const int i = threadIdx.x / LR;
+  const int64_t t0 = (int64_t)blockIdx.x * kv::kTok;
+  p.t = t0 + i;
   p.l = threadIdx.x % LR;
-  p.t = p.row / (uint32_t)a.H;
-  p.h = (int)(p.row - p.t * (uint32_t)a.H);
+  p.h0 = blockIdx.z * a.heads;
+  p.h1 = min(a.H, p.h0 + a.heads);
+  // a slot outside the cache is left out: negative (a padded row), or beyond it (an error)
+  int64_t slot = -1;
+  if (p.t < a.T) slot = __ldg(a.slots + p.t);
+  const int64_t first = __ldg(a.slots + t0);
+  if (slot >= a.total_slots) {
+    atomicOr(&g_device_error, kErrIndex);
+    slot = -1;
+  }
+  p.live = slot >= 0;
+  const int64_t page = slot >> a.page_shift;
+  const int in_page = (int)slot & ((1 << a.page_shift) - 1);
+  p.gran = (page * a.H << (a.page_shift - 4)) + in_page / kv::kTok;
+  p.tok = in_page % kv::kTok;
+  p.whole = __syncthreads_and(p.live && slot - i == first && first % kv::kTok == 0);
   return p;
 }
 
-// Start of the granule that holds `slot` of head h, and the token's place in it;
-// false for a slot outside the cache (negative: a padded row, else an error).
-__device__ __forceinline__ bool granule_of(const KvArgs &a, int64_t slot, int h, int granule, int64_t *off, int *tok) {
-  if (slot < 0) return false;
-  if (slot >= a.total_slots) {
-    atomicOr(&g_device_error, kErrIndex);
-    return false;
+// The keys' or values' part of a granule as one buffer: codes, then metadata.
+template <int BITS, int D, int GS>
+struct Part {
+  static constexpr int kCode = kv::layout(BITS, D, GS).code_bytes, kMeta = 64 * (D / GS), kBytes = kCode + kMeta;
+  static constexpr int kGranule = kv::layout(BITS, D, GS).granule;
+  // address of byte i of the buffer in the granule
+  static __device__ __forceinline__ unsigned char *at(unsigned char *gran, bool val, int i) {
+    return i < kCode ? gran + (val ? kCode : 0) + i : gran + 2 * kCode + (val ? kMeta : 0) + (i - kCode);
   }
-  const int64_t page = slot >> a.page_shift;
-  const int in_page = (int)slot & ((1 << a.page_shift) - 1);
-  *off = (((page * a.H + h) << a.page_shift) + in_page) / kv::kTok * granule;
-  *tok = in_page % kv::kTok;
-  return true;
-}
+  // byte offsets in the codes, and in the metadata
+  static __device__ __forceinline__ int word(int tok, int w) {
+    constexpr kv::Layout l = kv::layout(BITS, D, GS);
+    return kv::key_word(l, tok, w);
+  }
+  static __device__ __forceinline__ int half(int tok, int h) {
+    constexpr kv::Layout l = kv::layout(BITS, D, GS);
+    return kv::val_half(l, tok, h) - kCode;
+  }
+  static __device__ __forceinline__ int kmeta(int tok, int g) {
+    constexpr kv::Layout l = kv::layout(BITS, D, GS);
+    return kv::key_meta(l, tok, g) - 2 * kCode;
+  }
+  static __device__ __forceinline__ int vscale(int tok, int g) {
+    constexpr kv::Layout l = kv::layout(BITS, D, GS);
+    return kv::val_scale(l, tok, g) - 2 * kCode - kMeta;
+  }
+  static __device__ __forceinline__ int vbias(int tok, int g) {
+    constexpr kv::Layout l = kv::layout(BITS, D, GS);
+    return kv::val_bias(l, tok, g) - 2 * kCode - kMeta;
+  }
+};
 
-template <int BITS, int D, int GS, bool F16>
-__global__ void __launch_bounds__(kThreads) k_kv_write(const KvArgs a) {
-  constexpr kv::Layout L = kv::layout(BITS, D, GS);
-  constexpr int LG = GS / 8;              // lanes of a group
+// Quantizes kE elements of a row whose group lies on LG neighbouring threads.
+template <int BITS, int LG>
+__device__ __forceinline__ void quantize(const float (&v)[kE], uint32_t (&words)[kE * BITS / 32], float &s, float &mn) {
   constexpr float QMAX = (float)((1 << BITS) - 1);
-  const Place p = place_of<D>(a);
-  const bool val = blockIdx.y != 0;
-  int64_t off = 0;
-  int tok = 0;
-  const bool live = p.row < a.rows && granule_of(a, __ldg(a.slots + p.t), p.h, L.granule, &off, &tok);
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (live) {
-    const uint16_t *row = val ? a.v + p.t * a.v_stride : a.k + p.t * a.k_stride;
-    unpack8<F16>(__ldg(reinterpret_cast<const uint4 *>(row + p.h * D + p.l * 8)), v);
-  }
   // (min and max order -0 below +0, as qpack_affine's keys do)
-  float mn = v[0], mx = v[0];
+  float mx = v[0];
+  mn = v[0];
 #pragma unroll
-  for (int j = 1; j < 8; j++) {
+  for (int j = 1; j < kE; j++) {
     mn = fminf(mn, v[j]);
     mx = fmaxf(mx, v[j]);
   }
@@ -109,127 +139,204 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const KvArgs a) {
     mn = fminf(mn, __shfl_xor_sync(kFull, mn, o));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
   }
-  if (!live) return;
-  const float s = __fdiv_rn(__fsub_rn(mx, mn), QMAX);
+  s = quotient_const<(1 << BITS) - 1>(__fsub_rn(mx, mn));
   const Divisor d = make_divisor(s);
-  uint32_t words[BITS / 4];
   if (d.fast) {
-    // integers n in the low bits of the rounded quotients; no code passes QMAX (quotients are within 2^-23 of it)
-    float z[8];
+    // integers in the low bits of the rounded quotients; no code passes QMAX (quotients are within 2^-23 of it)
+    float z[kE];
 #pragma unroll
-    for (int j = 0; j < 8; j++) z[j] = round_bits(quotient_fast(__fsub_rn(v[j], mn), d));
+    for (int j = 0; j < kE; j++) z[j] = round_bits(quotient_fast(__fsub_rn(v[j], mn), d));
     if constexpr (BITS == 8) {
 #pragma unroll
-      for (int i = 0; i < 2; i++)
+      for (int i = 0; i < kE / 4; i++)
         words[i] = __byte_perm(__byte_perm(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]), 0x0040),
                                __byte_perm(__float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3]), 0x0040), 0x5410);
     } else {
       // four nibbles at a time in fp32: exact below 2^16
-      uint32_t h[2];
+      uint32_t h[kE / 4];
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
+      for (int i = 0; i < kE / 4; i++) {
         float n[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) n[j] = __fsub_rn(z[4 * i + j], kRoundMagic);
         h[i] = __float_as_uint(round_bits(fmaf(fmaf(n[3], 16.0f, n[2]), 256.0f, fmaf(n[1], 16.0f, n[0]))));
       }
-      words[0] = __byte_perm(h[0], h[1], 0x5410);
+#pragma unroll
+      for (int i = 0; i < kE / 8; i++) words[i] = __byte_perm(h[2 * i], h[2 * i + 1], 0x5410);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < BITS / 4; i++) words[i] = 0;
+    for (int i = 0; i < kE * BITS / 32; i++) words[i] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
+    for (int j = 0; j < kE; j++) {
       uint32_t q = 0;
       if (s != 0.0f) q = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[j], mn), s)), 0.0f), QMAX);
       words[j * BITS / 32] |= q << (j * BITS % 32);
     }
   }
-  unsigned char *gran = a.cache + off;
+}
+
+template <int BITS, int D, int GS, bool F16>
+__global__ void __launch_bounds__(D) k_kv_write(const KvArgs a) {
+  using P = Part<BITS, D, GS>;
+  constexpr int LG = GS / kE;             // threads of a group
+  constexpr int W = kE * BITS / 32;       // words of a thread
+  __shared__ __align__(16) unsigned char buf[2][P::kBytes];
+  const Place p = place_of<D>(a);
+  const bool val = blockIdx.y != 0;
+  const int64_t head_bytes = ((int64_t)P::kGranule << a.page_shift) / kv::kTok;
+  unsigned char *gran = a.cache + p.gran * P::kGranule + p.h0 * head_bytes;
+  const uint16_t *row = (val ? a.v + p.t * a.v_stride : a.k + p.t * a.k_stride) + p.l * kE + (int64_t)p.h0 * D;
+  uint4 next[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  auto fetch = [&]() {
+    next[0] = __ldg(reinterpret_cast<const uint4 *>(row));
+    next[1] = __ldg(reinterpret_cast<const uint4 *>(row) + 1);
+  };
+  if (p.live) fetch();
+  for (int h = p.h0; h < p.h1; h++, gran += head_bytes) {
+    float v[kE], s, mn;
+    unpack8<F16>(next[0], v);
+    unpack8<F16>(next[1], v + 8);
+    row += D;
+    if (p.live && h + 1 < p.h1) fetch();
+    uint32_t words[W];
+    quantize<BITS, LG>(v, words, s, mn);
+    // the units of this thread, into the buffer or straight into the cache
+    unsigned char *b = buf[h & 1];
+    auto put = [&](unsigned char *codes, unsigned char *meta) {   // where the codes and the metadata begin
+      const int g = p.l / LG;
+      if (!val) {
 #pragma unroll
-  for (int i = 0; i < BITS / 4; i++) {
-    const int w = p.l * (BITS / 4) + i;
-    if (!val) {
-      *reinterpret_cast<uint32_t *>(gran + kv::key_word(L, tok, w)) = words[i];
-    } else {
-      *reinterpret_cast<uint16_t *>(gran + kv::val_half(L, tok, 2 * w)) = (uint16_t)words[i];
-      *reinterpret_cast<uint16_t *>(gran + kv::val_half(L, tok, 2 * w + 1)) = (uint16_t)(words[i] >> 16);
-    }
-  }
-  if (p.l % LG == 0) {
-    const int g = p.l / LG;
-    if (!val) {
-      *reinterpret_cast<uint32_t *>(gran + kv::key_meta(L, tok, g)) = bf16_bits(s) | (bf16_bits(mn) << 16);
-    } else {
-      *reinterpret_cast<uint16_t *>(gran + kv::val_scale(L, tok, g)) = (uint16_t)bf16_bits(s);
-      *reinterpret_cast<uint16_t *>(gran + kv::val_bias(L, tok, g)) = (uint16_t)bf16_bits(mn);
+        for (int i = 0; i < W; i++) *reinterpret_cast<uint32_t *>(codes + P::word(p.tok, p.l * W + i)) = words[i];
+        if (p.l % LG == 0)
+          *reinterpret_cast<uint32_t *>(meta + P::kmeta(p.tok, g)) = bf16_bits(s) | (bf16_bits(mn) << 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+          const int w = p.l * W + i;
+          *reinterpret_cast<uint16_t *>(codes + P::half(p.tok, 2 * w)) = (uint16_t)words[i];
+          *reinterpret_cast<uint16_t *>(codes + P::half(p.tok, 2 * w + 1)) = (uint16_t)(words[i] >> 16);
+        }
+        if (p.l % LG == 0) {
+          *reinterpret_cast<uint16_t *>(meta + P::vscale(p.tok, g)) = (uint16_t)bf16_bits(s);
+          *reinterpret_cast<uint16_t *>(meta + P::vbias(p.tok, g)) = (uint16_t)bf16_bits(mn);
+        }
+      }
+    };
+    if (p.whole) {
+      put(b, b + P::kCode);
+      __syncthreads();                    // (the other buffer's readers have passed the barrier in front)
+      for (int i = threadIdx.x; i < P::kBytes / 16; i += D)
+        *reinterpret_cast<uint4 *>(P::at(gran, val, i * 16)) = reinterpret_cast<const uint4 *>(b)[i];
+    } else if (p.live) {
+      put(P::at(gran, val, 0), P::at(gran, val, P::kCode));
     }
   }
 }
 
 template <int BITS, int D, int GS, bool F16>
-__global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a) {
-  constexpr kv::Layout L = kv::layout(BITS, D, GS);
+__global__ void __launch_bounds__(D) k_kv_read(const KvArgs a) {
+  using P = Part<BITS, D, GS>;
+  __shared__ __align__(16) unsigned char buf[2][P::kBytes];
+  constexpr int kPer = (P::kBytes / 16 + D - 1) / D, W = kE * BITS / 32;
   const Place p = place_of<D>(a);
-  if (p.row >= a.rows) return;
   const bool val = blockIdx.y != 0;
-  int64_t off = 0;
-  int tok = 0;
-  uint32_t o[4] = {0, 0, 0, 0};
-  if (granule_of(a, __ldg(a.slots + p.t), p.h, L.granule, &off, &tok)) {
-    const unsigned char *gran = a.cache + off;
-    uint32_t words[BITS / 4];
-    const int g = p.l / (GS / 8);
-    float s, b;
-    if (!val) {
+  const int64_t head_bytes = ((int64_t)P::kGranule << a.page_shift) / kv::kTok;
+  unsigned char *gran = a.cache + p.gran * P::kGranule + p.h0 * head_bytes;
+  uint16_t *dst = (val ? a.vo : a.ko) + (p.t * a.H + p.h0) * D + p.l * kE;
+  uint4 next[kPer];
+  auto fetch = [&]() {
 #pragma unroll
-      for (int i = 0; i < BITS / 4; i++)
-        words[i] = *reinterpret_cast<const uint32_t *>(gran + kv::key_word(L, tok, p.l * (BITS / 4) + i));
-      const uint32_t m = *reinterpret_cast<const uint32_t *>(gran + kv::key_meta(L, tok, g));
-      s = bf16_lo(m);
-      b = bf16_hi(m);
-    } else {
+    for (int k = 0; k < kPer; k++) {
+      const int i = threadIdx.x + k * D;
+      if (i < P::kBytes / 16) next[k] = __ldg(reinterpret_cast<const uint4 *>(P::at(gran, val, i * 16)));
+    }
+  };
+  if (p.whole) fetch();
+  for (int h = p.h0; h < p.h1; h++, dst += D) {
+    unsigned char *b = buf[h & 1];
+    const unsigned char *here = gran;
+    if (p.whole) {
 #pragma unroll
-      for (int i = 0; i < BITS / 4; i++) {
-        const int w = p.l * (BITS / 4) + i;
-        words[i] = (uint32_t)*reinterpret_cast<const uint16_t *>(gran + kv::val_half(L, tok, 2 * w)) |
-                   (uint32_t)*reinterpret_cast<const uint16_t *>(gran + kv::val_half(L, tok, 2 * w + 1)) << 16;
+      for (int k = 0; k < kPer; k++) {
+        const int i = threadIdx.x + k * D;
+        if (i < P::kBytes / 16) reinterpret_cast<uint4 *>(b)[i] = next[k];
       }
-      s = bf16_lo(*reinterpret_cast<const uint16_t *>(gran + kv::val_scale(L, tok, g)));
-      b = bf16_lo(*reinterpret_cast<const uint16_t *>(gran + kv::val_bias(L, tok, g)));
     }
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      // a code in the low bits of 2^23's significand, made a number by a subtraction (exact)
-      const uint32_t q = ((words[j * BITS / 32] >> (j * BITS % 32)) & ((1u << BITS) - 1u)) | 0x4b000000u;
-      f[j] = __fmaf_rn(__fsub_rn(__uint_as_float(q), 8388608.0f), s, b);   // fp32(code * scale + bias)
+    gran += head_bytes;
+    if (p.whole) {
+      if (h + 1 < p.h1) fetch();
+      __syncthreads();                    // (the other buffer's readers have passed the barrier in front)
     }
+    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (p.live) {
+      uint32_t words[W];
+      float s, m;
+      auto get = [&](const unsigned char *codes, const unsigned char *meta) {
+        const int g = p.l / (GS / kE);
+        if (!val) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
-        o[j] = *reinterpret_cast<const uint32_t *>(&h);
+          for (int i = 0; i < W; i++) words[i] = *reinterpret_cast<const uint32_t *>(codes + P::word(p.tok, p.l * W + i));
+          const uint32_t u = *reinterpret_cast<const uint32_t *>(meta + P::kmeta(p.tok, g));
+          s = bf16_lo(u);
+          m = bf16_hi(u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; i++) {
+            const int w = p.l * W + i;
+            words[i] = (uint32_t)*reinterpret_cast<const uint16_t *>(codes + P::half(p.tok, 2 * w)) |
+                       (uint32_t)*reinterpret_cast<const uint16_t *>(codes + P::half(p.tok, 2 * w + 1)) << 16;
+          }
+          s = bf16_lo(*reinterpret_cast<const uint16_t *>(meta + P::vscale(p.tok, g)));
+          m = bf16_lo(*reinterpret_cast<const uint16_t *>(meta + P::vbias(p.tok, g)));
+        }
+      };
+      if (p.whole) {
+        get(b, b + P::kCode);
       } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-        o[j] = *reinterpret_cast<const uint32_t *>(&h);
+        unsigned char *from = const_cast<unsigned char *>(here);
+        get(P::at(from, val, 0), P::at(from, val, P::kCode));
       }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          // a code in the low bits of 2^23's significand, made a number by a subtraction (exact)
+          const int i = 2 * j + e;
+          const uint32_t q = ((words[i * BITS / 32] >> (i * BITS % 32)) & ((1u << BITS) - 1u)) | 0x4b000000u;
+          f[e] = __fmaf_rn(__fsub_rn(__uint_as_float(q), 8388608.0f), s, m);   // fp32(code * scale + bias)
+        }
+        if constexpr (F16) {
+          const __half2 x = __floats2half2_rn(f[0], f[1]);
+          o[j] = *reinterpret_cast<const uint32_t *>(&x);
+        } else {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]);
+          o[j] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+      }
+    }
+    if (p.t < a.T) {
+      reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
-  uint16_t *dst = (val ? a.vo : a.ko) + (int64_t)p.row * D + p.l * 8;
-  *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int BITS, int D, int GS>
-void launch(const KvArgs &a, bool f16, bool write, cudaStream_t st) {
-  constexpr uint32_t per = kThreads / (D / 8);          // rows of a block
-  const dim3 grid((a.rows + per - 1) / per, 2);
+void launch(KvArgs a, bool f16, bool write, cudaStream_t st) {
+  // heads in turn only where the tokens alone fill the GPU: 8 blocks an SM
+  const int64_t tiles = (a.T + kv::kTok - 1) / kv::kTok;
+  int64_t z = (148 * 8 + 2 * tiles - 1) / (2 * tiles);
+  z = z < 1 ? 1 : (z > a.H ? a.H : z);
+  a.heads = (int)((a.H + z - 1) / z);
+  const dim3 grid((unsigned)tiles, 2, (unsigned)((a.H + a.heads - 1) / a.heads));
   if (write) {
-    if (f16) k_kv_write<BITS, D, GS, true><<<grid, kThreads, 0, st>>>(a);
-    else k_kv_write<BITS, D, GS, false><<<grid, kThreads, 0, st>>>(a);
+    if (f16) k_kv_write<BITS, D, GS, true><<<grid, D, 0, st>>>(a);
+    else k_kv_write<BITS, D, GS, false><<<grid, D, 0, st>>>(a);
   } else {
-    if (f16) k_kv_read<BITS, D, GS, true><<<grid, kThreads, 0, st>>>(a);
-    else k_kv_read<BITS, D, GS, false><<<grid, kThreads, 0, st>>>(a);
+    if (f16) k_kv_read<BITS, D, GS, true><<<grid, D, 0, st>>>(a);
+    else k_kv_read<BITS, D, GS, false><<<grid, D, 0, st>>>(a);
   }
 }
 
@@ -253,7 +360,7 @@ void launch_kv_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int
                      int64_t T, const KvCache &c, bool f16, cudaStream_t st) {
   KvArgs a{};
   a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride;
-  a.slots = slots; a.rows = (uint32_t)(T * c.heads);
+  a.slots = slots; a.T = T;
   a.cache = static_cast<unsigned char *>(c.data);
   a.total_slots = c.pages * c.page_size;
   a.H = (int)c.heads;
@@ -265,7 +372,7 @@ void launch_kv_read(const KvCache &c, const int64_t *slots, int64_t T, uint16_t 
                     cudaStream_t st) {
   KvArgs a{};
   a.ko = k; a.vo = v;
-  a.slots = slots; a.rows = (uint32_t)(T * c.heads);
+  a.slots = slots; a.T = T;
   a.cache = static_cast<unsigned char *>(c.data);
   a.total_slots = c.pages * c.page_size;
   a.H = (int)c.heads;

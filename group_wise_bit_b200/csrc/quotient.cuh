@@ -32,6 +32,15 @@ __device__ __forceinline__ float quotient_fast(float a, const Divisor &d) {
   return __fmaf_rn(__fmaf_rn(-q, d.b, a), d.y, q);
 }
 
+// a / N for a constant N (neither a power of two nor of an all-ones significand), correctly rounded.
+template <int N>
+__device__ __forceinline__ float quotient_const(float a) {
+  constexpr float b = (float)N, y = 1.0f / (float)N;
+  if (!(a >= 0x1p-90f && a <= 0x1p120f)) return __fdiv_rn(a, b);
+  const float q = __fmul_rn(a, y);
+  return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+}
+
 // Round half to even of |x| <= 2^22 as the low bits of a float (two's complement from bit 0).
 constexpr float kRoundMagic = 12582912.0f;   // 1.5 * 2^23
 __device__ __forceinline__ float round_bits(float x) { return __fadd_rn(x, kRoundMagic); }

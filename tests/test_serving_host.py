@@ -96,8 +96,6 @@ def test_write_and_read_refusals():
     assert read(k=NULL) == 1 and read(v=NULL) == 1 and read(slots=NULL) == 1 and read(cache=NULL) == 1
     assert read(k=OK8) == 4 and read(v=OK8) == 4 and read(cache=BAD) == 4
     assert read(T=0, k=NULL, v=NULL, slots=NULL, cache=NULL) == 0
-    # more (token, head) rows than 32 bits number
-    assert _st("gwb_kv_read", OK16, 4, 65535, 16, 256, 4, 32, OK16, 1 << 16, 0, OK16, OK16, NULL) == 2
 
 
 def test_attention_refusals():
