@@ -384,6 +384,11 @@ def _out_like(t, name, like, dtype):
     return torch.empty_like(like, dtype=dtype) if t is None else _dev(t, name, (dtype,), like.shape)
 
 
+def _out_of(t, name, src, shape, dtype):
+    """_out on src's device (less host time than torch.empty)."""
+    return src.new_empty(shape, dtype=dtype) if t is None else _dev(t, name, (dtype,), shape)
+
+
 def _token_rows(t, name, shape, dtypes):
     """Rows [T, heads, head_dim] whose heads are contiguous; returns the elements between tokens."""
     if not isinstance(t, torch.Tensor):
@@ -416,7 +421,7 @@ def rmsnorm_quant_i8(x, weight, eps, residual=None, residual_out=None, qx=None, 
     elif residual_out is not None:
         raise ValueError("residual_out without residual: the sum would be x itself")
     qx = _out_like(qx, "qx", x, torch.int8)
-    sx = _out(sx, "sx", (M,), torch.float32, x.device)
+    sx = _out_of(sx, "sx", x, (M,), torch.float32)
     _here(x, weight, residual, residual_out, qx, sx)
     _call("gwb_rmsnorm_quant_i8", _ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _HALF[x.dtype],
           _ptr(residual_out), _ptr(qx), _ptr(sx), _stream())
@@ -463,7 +468,7 @@ def _cache_check(cache, head_dim, bits, group_size):
     if cache.dim() != 3:
         raise ValueError(f"cache: shape {tuple(cache.shape)} != [pages, heads, block]")
     pages, heads, block = cache.shape
-    granule = kv_block_bytes(16, head_dim, bits, group_size)
+    granule = _block_bytes.get((16, head_dim, bits, group_size)) or kv_block_bytes(16, head_dim, bits, group_size)
     if block % granule != 0:
         raise ValueError(f"cache: a block of {block} bytes does not hold granules of {granule} bytes "
                          f"(head_dim {head_dim}, {bits} bits, group size {group_size})")
@@ -492,9 +497,10 @@ def kv_read(cache, slots, head_dim, bits, group_size, dtype=torch.bfloat16, k=No
     if dtype not in _HALF:
         raise TypeError(f"dtype {dtype} not in {tuple(_HALF)}")
     _dev(slots, "slots", (torch.int64,))
-    shape = (slots.numel(), heads, head_dim)
-    _dev(slots, "slots", (torch.int64,), shape[:1])
-    k = _out(k, "k", shape, dtype, cache.device)
+    if slots.dim() != 1:
+        raise ValueError(f"slots: shape {tuple(slots.shape)} != [tokens]")
+    shape = (slots.shape[0], heads, head_dim)
+    k = _out_of(k, "k", cache, shape, dtype)
     v = _out_like(v, "v", k, dtype)
     _here(cache, slots, k, v)
     _call("gwb_kv_read", _ptr(cache), pages, heads, page_size, head_dim, bits, group_size, _ptr(slots), shape[0],
@@ -539,13 +545,13 @@ def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, ou
     if B > 1 and page_table.stride(0) < max_pages:
         raise ValueError("page_table: rows overlap")
     _dev(seq_lens, "seq_lens", (torch.int32,), (B,))
-    out = _out(out, "out", (B, HQ, D), q.dtype, q.device)
+    out = _out_of(out, "out", q, (B, HQ, D), q.dtype)
     if lse is not None:
         _dev(lse, "lse", (torch.float32,), (B, HQ))
     _here(q, cache, page_table, seq_lens, out, lse, workspace)
-    need = attn_decode_workspace(HQ, heads, D)
+    need = _ws_bytes.get((q.get_device(), HQ, heads, D)) or attn_decode_workspace(HQ, heads, D)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = cache.new_empty(need)
     else:
         _dev(workspace, "workspace", (torch.uint8,))
     _call("gwb_attn_decode", _ptr(q), qs, B, HQ, _HALF[q.dtype], _ptr(cache), pages, heads, page_size, D, bits,
