@@ -223,7 +223,7 @@ struct Cursor {
   int g, end;                   // units [g, end) of the piece are left to this walker
   int len;                      // tokens of the sequence
   long long left;               // places of the share behind this piece
-  const unsigned char *head;    // the pair's head in page 0
+  int head;                     // granules of a page in front of the pair's head
   const int32_t *row;           // the sequence's page ids
   int page0, page1;             // page ids of unit g's granules (loaded one unit ahead)
 };
@@ -249,7 +249,7 @@ __device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int
       c.left -= len;
       c.end = g + len;
       c.g = g + first;
-      c.head = a.cache + (((int64_t)(c.hc / a.chunks)) << a.gshift) * GB;
+      c.head = (c.hc / a.chunks) << a.gshift;
       c.row = a.table + (int64_t)c.b * a.table_stride;
       if constexpr (PAGES) cursor_page(a, c);
       return true;
@@ -783,47 +783,50 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   cursor_settle<K::GB>(a, cp, way);
   if (tid == 0 && a.mode == kCut) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
 
-  uint32_t filled = 0, phase = 0;     // slots with a copy, parity of each slot's next wait
+  // The ring: units go in and out in order, slot after slot.  A slot's barrier completes a phase for every
+  // unit, also for one without a copy, so that one parity serves all slots of a round.
+  int slot_in = 0, slot_out = 0, flying = 0;
+  uint32_t parity = 0;
   uint32_t lack0 = 0, lack1 = 0;      // slots without their first / second granule
-  int slot_in = 0, slot_out = 0;
   bool dead = false;
-  const int64_t page_bytes = ((int64_t)a.H << a.gshift) * K::GB;
+  const uint32_t page_gran = (uint32_t)a.H << a.gshift;     // granules of a page
   auto issue = [&]() {                // the cursor's unit into slot_in
     if (cp.g >= cp.end) return;
     // the second granule only where a token of it is in front of the length (its page may not exist)
     const bool two = cp.g * kUnit + kv::kTok < cp.len;
-    unsigned char *dst = ring + slot_in * 2 * K::GB;
+    unsigned char *dst = ring + slot_in * (2 * K::GB);
     uint64_t *full = bar + slot_in;
-    const uint32_t bit = 1u << slot_in;
+    // granule of the cache
+    auto gran = [&](int page) {
+      return a.cache + ((int64_t)page * page_gran + (cp.head + (cp.g * 2 & ((1 << a.gshift) - 1)))) * K::GB;
+    };
     if (max((uint32_t)cp.page0, (uint32_t)cp.page1) < (uint32_t)a.pages) {
       if (lane == 0) {
-        const unsigned char *src = cp.head + cp.page0 * page_bytes + (cp.g * 2 & ((1 << a.gshift) - 1)) * K::GB;
         const uint32_t bytes = two ? 2 * K::GB : K::GB;
         mbar_arrive_expect_tx(full, bytes);
         if (a.gshift != 0) {                     // both in one page
-          bulk_load(dst, src, bytes, full);
+          bulk_load(dst, gran(cp.page0), bytes, full);
         } else {
-          bulk_load(dst, src, K::GB, full);
-          if (two) bulk_load(dst + K::GB, cp.head + cp.page1 * page_bytes, K::GB, full);
+          bulk_load(dst, gran(cp.page0), K::GB, full);
+          if (two) bulk_load(dst + K::GB, gran(cp.page1), K::GB, full);
         }
       }
-      filled |= bit;
     } else {                                     // a granule whose page is outside the cache is left out and reported
       const bool ok0 = (uint32_t)cp.page0 < (uint32_t)a.pages, ok1 = two && (uint32_t)cp.page1 < (uint32_t)a.pages;
       if (lane == 0) {
         atomicOr(&g_device_error, kErrIndex);
-        if (ok0 || ok1) mbar_arrive_expect_tx(full, K::GB);
-        if (ok0) bulk_load(dst, cp.head + cp.page0 * page_bytes, K::GB, full);      // (gshift 0: else both are bad)
-        if (ok1) bulk_load(dst + K::GB, cp.head + cp.page1 * page_bytes, K::GB, full);
+        mbar_arrive_expect_tx(full, ok0 || ok1 ? K::GB : 0);
+        if (ok0) bulk_load(dst, gran(cp.page0), K::GB, full);      // (gshift 0: else both are bad)
+        if (ok1) bulk_load(dst + K::GB, gran(cp.page1), K::GB, full);
       }
-      if (ok0 || ok1) filled |= bit;
-      if (!ok0) lack0 |= bit;
-      if (!ok1) lack1 |= bit;
+      if (!ok0) lack0 |= 1u << slot_in;
+      if (!ok1) lack1 |= 1u << slot_in;
     }
-    slot_in = slot_in + 1 == a.depth ? 0 : slot_in + 1;
+    flying++;
+    if (++slot_in == a.depth) slot_in = 0;
     cp.g += ways;
     cursor_page(a, cp);
-    cursor_settle<K::GB>(a, cp, way);
+    if (cp.g >= cp.end) cursor_settle<K::GB>(a, cp, way);
   };
   // (a warp alone keeps its queries in its part of the join buffer, which it writes after it has read them)
   unsigned char *qbuf = alone ? reinterpret_cast<unsigned char *>(join + warp * K::GHP * K::SROW) : qcta;
@@ -925,31 +928,32 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     if (more) fetch_q(nc);            // (in flight through the piece's loop)
 
     // ---- this warp's units of the piece
-    for (int g = g_first + way; g < pc.end; g += ways) {
-      if ((filled >> slot_out & 1u) && !dead) {
-        if (mbar_wait(bar + slot_out, phase >> slot_out & 1u)) {
-          unsigned char *sm = ring + slot_out * 2 * K::GB;
-          int lo = 0, valid = pc.len - g * kUnit;
-          if ((lack0 | lack1) >> slot_out & 1u) {
-            if (lack0 >> slot_out & 1u) lo = kv::kTok;
-            if (lack1 >> slot_out & 1u) valid = min(valid, kv::kTok);
-          }
-          if (lo > 0 || valid < kUnit) {
-            K::clear_tail(sm, lo > 0 ? 0 : valid);
-            K::clear_tail(sm + K::GB, valid - kv::kTok);
-          }
-          K::unit(sm, meta, lo, valid, qf, qsum, sf, s);
-          phase ^= 1u << slot_out;
-          filled &= ~(1u << slot_out);
-        } else {
-          dead = true;
+    for (int g = g_first + way; g < pc.end && !dead; g += ways) {
+      if (!mbar_wait(bar + slot_out, parity)) {
+        dead = true;
+        break;
+      }
+      flying--;
+      unsigned char *sm = ring + slot_out * (2 * K::GB);
+      int lo = 0, valid = pc.len - g * kUnit;
+      if (valid < kUnit || (lack0 | lack1)) {        // a last unit, or one of few with a page outside the cache
+        const uint32_t bit = 1u << slot_out;
+        if (lack0 & bit) lo = kv::kTok;
+        if (lack1 & bit) valid = min(valid, kv::kTok);
+        lack0 &= ~bit;
+        lack1 &= ~bit;
+        if (lo < valid) {
+          if (lo > 0 || valid < kv::kTok) K::clear_tail(sm, lo > 0 ? 0 : valid);
+          if (valid < kUnit) K::clear_tail(sm + K::GB, valid - kv::kTok);
         }
       }
+      if (lo < valid) K::unit(sm, meta, lo, valid, qf, qsum, sf, s);
       __syncwarp();
-      lack0 &= ~(1u << slot_out);
-      lack1 &= ~(1u << slot_out);
-      slot_out = slot_out + 1 == a.depth ? 0 : slot_out + 1;
-      if (!dead) issue();
+      if (++slot_out == a.depth) {
+        slot_out = 0;
+        parity ^= 1u;
+      }
+      issue();
     }
 
     // ---- join the warps: row h of every warp's sums, scaled to the common max
@@ -1011,9 +1015,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     g_first = 0;
   }
   // copies still in flight (only after a wait gave up) land before the CTA's memory is freed
-  if (dead)
-    for (int i = 0; i < a.depth; i++)
-      if (filled >> i & 1u) mbar_wait(bar + i, phase >> i & 1u);
+  for (; flying > 0; flying--) {
+    mbar_wait(bar + slot_out, parity);
+    if (++slot_out == a.depth) {
+      slot_out = 0;
+      parity ^= 1u;
+    }
+  }
 }
 
 // Joins the pieces of a pair that shares cut.  Block i looks at the boundary in
