@@ -369,14 +369,16 @@ def gemm_i8i8(qx, sx, wq, sw, want_y=True, want_acc=False, y=None, acc=None):
 
 # ------------------------------------------------------------------ norm, quantized paged cache, decode attention
 _HALF = {torch.bfloat16: 0, torch.float16: 1}   # gwb_dtype
+_HALVES = tuple(_HALF)
 
 
-def _here(*tensors):
-    """All given tensors lie on the current CUDA device (the one whose stream the call goes to)."""
+def _stream_of(*tensors):
+    """The current stream; all given tensors must lie on its device, the current one."""
     cur = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+    return _stream()
 
 
 def _out_like(t, name, like, dtype):
@@ -396,7 +398,7 @@ def _token_rows(t, name, shape, dtypes):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.dim() != 3 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape) if shape else '[tokens, heads, head_dim]'}")
     T, H, D = t.shape
@@ -411,7 +413,7 @@ def rmsnorm_quant_i8(x, weight, eps, residual=None, residual_out=None, qx=None, 
 
     x, residual bf16 or fp16 [M, K], weight [K] of the same dtype; h = x + residual, rounded once, is
     written to residual_out (which may be x or residual).  qx and sx are what gemm_i8i8 / gemm_i8i4 take."""
-    _dev(x, "x", tuple(_HALF))
+    _dev(x, "x", _HALVES)
     M, K = x.shape
     dt = (x.dtype,)
     _dev(weight, "weight", dt, (K,))
@@ -422,9 +424,9 @@ def rmsnorm_quant_i8(x, weight, eps, residual=None, residual_out=None, qx=None, 
         raise ValueError("residual_out without residual: the sum would be x itself")
     qx = _out_like(qx, "qx", x, torch.int8)
     sx = _out_of(sx, "sx", x, (M,), torch.float32)
-    _here(x, weight, residual, residual_out, qx, sx)
+    stream = _stream_of(x, weight, residual, residual_out, qx, sx)
     _call("gwb_rmsnorm_quant_i8", _ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _HALF[x.dtype],
-          _ptr(residual_out), _ptr(qx), _ptr(sx), _stream())
+          _ptr(residual_out), _ptr(qx), _ptr(sx), stream)
     return qx, sx, residual_out
 
 
@@ -434,10 +436,10 @@ def dequant_per_token_i8(qx, sx, dtype=torch.bfloat16, out=None):
     M, K = qx.shape
     _dev(sx, "sx", (torch.float32,), (M,))
     if dtype not in _HALF:
-        raise TypeError(f"dtype {dtype} not in {tuple(_HALF)}")
+        raise TypeError(f"dtype {dtype} not in {_HALVES}")
     out = _out_like(out, "out", qx, dtype)
-    _here(qx, sx, out)
-    _call("gwb_dequant_per_token_i8", _ptr(qx), _ptr(sx), M, K, _HALF[dtype], _ptr(out), _stream())
+    stream = _stream_of(qx, sx, out)
+    _call("gwb_dequant_per_token_i8", _ptr(qx), _ptr(sx), M, K, _HALF[dtype], _ptr(out), stream)
     return out
 
 
@@ -478,16 +480,16 @@ def _cache_check(cache, head_dim, bits, group_size):
 def kv_write(cache, slots, k, v, bits, group_size):
     """Quantizes k, v [T, heads, head_dim] (bf16 or fp16, any token stride) into the cache at slots
     (int64 [T], page * page_size + place; negative: the row is padding and left out)."""
-    ks = _token_rows(k, "k", None, _HALF)
+    ks = _token_rows(k, "k", None, _HALVES)
     T, H, D = k.shape
     vs = _token_rows(v, "v", k.shape, (k.dtype,))
     pages, heads, page_size = _cache_check(cache, D, bits, group_size)
     if heads != H:
         raise ValueError(f"k has {H} heads, the cache {heads}")
     _dev(slots, "slots", (torch.int64,), (T,))
-    _here(cache, slots, k, v)
+    stream = _stream_of(cache, slots, k, v)
     _call("gwb_kv_write", _ptr(k), ks, _ptr(v), vs, _ptr(slots), T, _HALF[k.dtype], _ptr(cache), pages, heads,
-          page_size, D, bits, group_size, _stream())
+          page_size, D, bits, group_size, stream)
     return cache
 
 
@@ -495,16 +497,16 @@ def kv_read(cache, slots, head_dim, bits, group_size, dtype=torch.bfloat16, k=No
     """The cache's rows at slots (int64 [T]) as dense k, v [T, heads, head_dim]; zeros for negative slots."""
     pages, heads, page_size = _cache_check(cache, head_dim, bits, group_size)
     if dtype not in _HALF:
-        raise TypeError(f"dtype {dtype} not in {tuple(_HALF)}")
+        raise TypeError(f"dtype {dtype} not in {_HALVES}")
     _dev(slots, "slots", (torch.int64,))
     if slots.dim() != 1:
         raise ValueError(f"slots: shape {tuple(slots.shape)} != [tokens]")
     shape = (slots.shape[0], heads, head_dim)
     k = _out_of(k, "k", cache, shape, dtype)
     v = _out_like(v, "v", k, dtype)
-    _here(cache, slots, k, v)
+    stream = _stream_of(cache, slots, k, v)
     _call("gwb_kv_read", _ptr(cache), pages, heads, page_size, head_dim, bits, group_size, _ptr(slots), shape[0],
-          _HALF[dtype], _ptr(k), _ptr(v), _stream())
+          _HALF[dtype], _ptr(k), _ptr(v), stream)
     return k, v
 
 
@@ -529,7 +531,7 @@ def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, ou
     stride), seq_lens int32 [B] (0: an empty row, zeros).  scale defaults to 1 / sqrt(head_dim).  lse, if
     given, is an fp32 [B, q_heads] output.  workspace: a uint8 tensor of attn_decode_workspace() bytes that
     no overlapping call uses; without one the call takes it from torch's allocator."""
-    qs = _token_rows(q, "q", None, _HALF)
+    qs = _token_rows(q, "q", None, _HALVES)
     B, HQ, D = q.shape
     pages, heads, page_size = _cache_check(cache, D, bits, group_size)
     if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
@@ -548,7 +550,7 @@ def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, ou
     out = _out_of(out, "out", q, (B, HQ, D), q.dtype)
     if lse is not None:
         _dev(lse, "lse", (torch.float32,), (B, HQ))
-    _here(q, cache, page_table, seq_lens, out, lse, workspace)
+    stream = _stream_of(q, cache, page_table, seq_lens, out, lse, workspace)
     need = _ws_bytes.get((q.get_device(), HQ, heads, D)) or attn_decode_workspace(HQ, heads, D)
     if workspace is None:
         workspace = cache.new_empty(need)
@@ -557,7 +559,7 @@ def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, ou
     _call("gwb_attn_decode", _ptr(q), qs, B, HQ, _HALF[q.dtype], _ptr(cache), pages, heads, page_size, D, bits,
           group_size, _ptr(page_table), ts, max_pages, _ptr(seq_lens),
           float(1.0 / D ** 0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(workspace),
-          workspace.numel(), _stream())
+          workspace.numel(), stream)
     return out
 
 

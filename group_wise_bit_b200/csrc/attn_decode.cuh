@@ -839,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     cp_async_commit();
   };
   fetch_q(pc);
-  for (int i = 0; i < a.depth; i++) issue();
+  issue();
+  int rest = a.depth - 1;             // first copies held back until the queries are staged: theirs come sooner
 
   typename K::State s;
   int g_first = pc.g;
@@ -926,6 +927,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     const bool more = cursor_next_piece<K::GB, false>(a, nc, 0);
     pair_sync();                      // every warp holds its queries
     if (more) fetch_q(nc);            // (in flight through the piece's loop)
+    for (; rest > 0; rest--) issue();
 
     // ---- this warp's units of the piece
     for (int g = g_first + way; g < pc.end && !dead; g += ways) {
