@@ -110,6 +110,9 @@ try:   # the raw handle of the current stream, without building a Stream object 
     def _stream():
         return _raw_stream(torch.cuda.current_device())
 except AttributeError:   # pragma: no cover - older torch
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
     def _stream():
         return torch.cuda.current_stream().cuda_stream
 
@@ -378,7 +381,7 @@ def _stream_of(*tensors):
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
-    return _stream()
+    return _raw_stream(cur)
 
 
 def _out_like(t, name, like, dtype):

@@ -4,6 +4,10 @@ Codes, scales, biases, int8 values and residual sums must be bit-exact with the 
 definitions state them); attention outputs must lie within the elementwise bound the oracle derives from
 fp32 scores, fp16 softmax weights and one output rounding (oracle.serving.attn_decode).
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -231,6 +235,26 @@ def test_cache_slots_outside_are_left_out_and_reported():
     gwb.check_device_error()
     assert gwb.kv_read(cache, slots[:0], 64, 4, 32)[0].shape == (0, 1, 64)
     gwb.kv_write(cache, slots[:0], k[:0], k[:0], 4, 32)
+
+
+def test_a_slot_named_twice_touches_nothing_else():
+    """Slots must be distinct; one named twice holds some mixture, and every other row is what it should be."""
+    rng = np.random.default_rng(40)
+    T, H, D = 64, 2, 128
+    k, v = _rand(rng, (T, H, D), "bf16"), _rand(rng, (T, H, D), "bf16")
+    slots = np.arange(T)
+    slots[[3, 20, 47]] = [50, 50, 21]
+    ref = _random_cache(rng, 5, H, D, 16, 4, 64)
+    cache = torch.tensor(ref).to(DEV)
+    gwb.kv_write(cache, torch.tensor(slots).to(DEV), _t(k, "bf16"), _t(v, "bf16"), 4, 64)
+    S.write_rows(ref, slots, k, "k", 4, 64, 16)
+    S.write_rows(ref, slots, v, "v", 4, 64, 16)
+    got = cache.cpu().numpy()
+    rest = np.setdiff1d(np.arange(80), [50, 21])
+    for what in "kv":
+        for a, b in zip(S.parts_of(got, rest, what, 4, D, 64, 16), S.parts_of(ref, rest, what, 4, D, 64, 16)):
+            assert np.array_equal(a, b, equal_nan=True)
+    gwb.check_device_error()
 
 
 def test_binding_refusals_on_the_gpu():
@@ -543,6 +567,39 @@ def test_a_captured_step_follows_lengths_and_cache():
         ref, _, bound, _ = S.attn_decode(b.q, cache.cpu().numpy(), b.table, n, bits, gs, 16, np.float64(np.float32(0.125)), False)
         assert (np.abs(_np(graph[0]) - ref) <= bound).all()
     gwb.check_device_error()
+
+
+def test_a_first_call_may_be_a_captured_one():
+    """A fresh process whose first calls of the library are made under stream capture."""
+    code = """
+import torch, group_wise_bit_b200 as gwb
+d = "cuda"
+cache = gwb.kv_cache(40, 2, 128, 32, 4, 64)
+k = torch.randn(3, 2, 128, device=d).bfloat16()
+slots = torch.tensor([0, 32, 1200], device=d)
+table = torch.arange(40, dtype=torch.int32, device=d)[None].repeat(3, 1).contiguous()
+lens = torch.tensor([1, 33, 1201], dtype=torch.int32, device=d)
+q = torch.randn(3, 8, 128, device=d).bfloat16()
+w = torch.ones(1024, dtype=torch.bfloat16, device=d)
+def step():
+    gwb.kv_write(cache, slots, k, k, 4, 64)
+    a = gwb.attn_decode(q, cache, table, lens, 4, 64)
+    b = gwb.attn_decode(q, cache, table[:, :4], lens.clamp(max=128), 4, 64)
+    return a, b, *gwb.rmsnorm_quant_i8(a.view(3, -1), w, 1e-5), *gwb.kv_read(cache, slots, 128, 4, 64)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+for x, y in zip(got, step()):
+    assert (x is None and y is None) or torch.equal(x, y)
+gwb.check_device_error()
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 def test_calls_on_two_streams_and_two_graphs_do_not_share_a_workspace():
