@@ -69,6 +69,7 @@ struct Args {
   int B, H, G, GH;              // GH: query heads of one chunk
   int chunks;                   // chunks of a kv head's G query heads
   int gshift, cap;              // log2 of a page's granules; tokens a table row can name
+  int ushift;                   // log2 of a unit's granules
   int depth;                    // ring slots a warp
   int min_per;                  // least places of a share
   int f16;
@@ -79,9 +80,10 @@ struct Args {
 // How pairs are spread: cut into equal shares; a CTA a pair; a warp a pair (no pair is cut in the last two).
 enum { kCut = 0, kCtaPair = 1, kWarpPair = 2 };
 
-// One record a CTA: the first piece of its share.
+// One record a CTA, for the join: the pair that the boundary in front of its share cuts, where no
+// earlier boundary does.
 struct Rec {
-  int b, hc, g0, n;             // sequence, head chunk, first unit, units of the sequence (0: no piece)
+  int b, hc, pieces, pad;       // sequence, head chunk, pieces of the pair from share i - 1 on (0: nothing to join)
 };
 // Workspace: [2 * CTAs] partials of GHP heads x (D sums, max, total), then [CTAs] Rec, then the share size.
 template <int D, int GHP>
@@ -156,12 +158,11 @@ __device__ __forceinline__ float q_at(const uint16_t *p, int f16) {
 // kPieceCost places begins at its unit 0; one that ends there leaves the pair
 // to the next share.
 constexpr int kPieceCost = 16;
-constexpr int kUnit = 2 * kv::kTok;   // tokens of a unit
 
 // Where the share of a CTA begins, and its length.
 struct Start {
   int b, hc, u, pad;             // sequence, head chunk and place in the pair
-  long long left;                // places of the share; 0: nothing to do
+  long long left, per;           // places of this share (0: nothing to do), of every share but the last
 };
 
 // Tokens of sequence b, cut to what its table row can name.
@@ -170,7 +171,10 @@ __device__ __forceinline__ int tokens(const Args &a, int b, bool report) {
   if (len > a.cap && report) atomicOr(&g_device_error, kErrIndex);
   return min(len, a.cap);
 }
-__device__ __forceinline__ int units(int len) { return len / kUnit + (len % kUnit != 0); }
+__device__ __forceinline__ int units(const Args &a, int len) {
+  const int s = 4 + a.ushift;
+  return (len >> s) + ((len & ((1 << s) - 1)) != 0);
+}
 __device__ __forceinline__ long long places(int n) { return n > 0 ? n + kPieceCost : 0; }
 
 // Every thread sums a run of the lengths, a scan joins them.
@@ -179,7 +183,7 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
   const int run = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
   long long mine = 0;
-  for (int b = b0; b < b1; b++) mine += places(units(tokens(a, b, blockIdx.x == 0)));
+  for (int b = b0; b < b1; b++) mine += places(units(a, tokens(a, b, blockIdx.x == 0)));
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -202,12 +206,13 @@ __device__ __forceinline__ void find_start(const Args &a, Start *st, long long *
   if (first < total && first >= before && first < before + mine * HC) {
     long long left = first - before;
     for (int b = b0; b < b1; b++) {
-      const long long n = places(units(tokens(a, b, false)));
+      const long long n = places(units(a, tokens(a, b, false)));
       if (left < n * HC) {
         st->b = b;
         st->hc = (int)(left / n);
         st->u = (int)(left - (long long)st->hc * n);
         st->left = min(per, total - first);
+        st->per = per;
         break;
       }
       left -= n * HC;
@@ -228,10 +233,15 @@ struct Cursor {
   int page0, page1;             // page ids of unit g's granules (loaded one unit ahead)
 };
 
+// Whether the unit has a second granule with a token in front of the length (else that one's page may not exist).
+__device__ __forceinline__ bool cursor_two(const Args &a, const Cursor &c) {
+  return a.ushift != 0 && (2 * c.g + 1) * kv::kTok < c.len;
+}
 __device__ __forceinline__ void cursor_page(const Args &a, Cursor &c) {
   if (c.g < c.end) {
-    c.page0 = c.page1 = __ldg(c.row + (c.g * 2 >> a.gshift));
-    if (a.gshift == 0 && c.g * kUnit + kv::kTok < c.len) c.page1 = __ldg(c.row + c.g * 2 + 1);
+    const int i = c.g << a.ushift;
+    c.page0 = c.page1 = __ldg(c.row + (i >> a.gshift));
+    if (a.gshift == 0 && cursor_two(a, c)) c.page1 = __ldg(c.row + i + 1);
   }
 }
 // Opens the piece at place u of (b, hc), skipping empty sequences; false when the share ends in front of it.
@@ -240,7 +250,7 @@ __device__ __forceinline__ bool cursor_open(const Args &a, Cursor &c, int u, int
   c.g = c.end = 0;
   while (c.left > 0 && c.b < a.B) {
     c.len = tokens(a, c.b, false);
-    c.n = units(c.len);
+    c.n = units(a, c.len);
     if (c.n > 0) {
       const int g = max(0, u - kPieceCost);
       c.left -= max(0, kPieceCost - u);
@@ -274,6 +284,10 @@ __device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int firs
   while (c.g >= c.end && c.left > 0) cursor_next_piece<GB>(a, c, first);
 }
 
+// Granules of a unit: two, for the sake of what a unit costs besides its tokens and of two independent chains of
+// products; one where two rings of two would leave an SM with one CTA (8 bits, head_dim 256).
+constexpr int unit_granules(int granule) { return granule > 8192 ? 1 : 2; }
+
 // Resident CTAs an SM that the registers are held to: 16 warps where 128
 // registers a thread hold the state, 8 where it takes more.
 constexpr int min_ctas(int D, int NT) { return D * NT <= 128 ? 3 : 2; }
@@ -283,6 +297,9 @@ struct Kernel {
   static constexpr kv::Layout L = kv::layout(BITS, D, GS);
   static constexpr int NG = L.NG;
   static constexpr int GB = L.granule;
+  static constexpr int UG = unit_granules(L.granule);     // granules of a unit
+  static constexpr int kUnit = UG * kv::kTok;             // tokens of a unit
+  static constexpr int kSlot = UG * GB;                   // bytes of a ring slot
   static constexpr int KM = D / 16;                       // score MMAs a granule and n-tile
   static constexpr int VB = BITS == 4 ? D / 32 : D / 16;  // value blocks (8 lanes x 16 bits a token)
   static constexpr int MPB = BITS == 4 ? 2 : 1;           // MMAs a value block
@@ -291,9 +308,9 @@ struct Kernel {
   static constexpr int SROW = D + 4;                      // floats of a head's row in the join buffer
   static constexpr int kJoin = kWarps * GHP * (SROW + 2) * 4;
 
-  // Pairs of tokens whose value scale and bias a lane converts a unit: word lane + 32 k of the
-  // unit's 16 NG, of granule i / (8 NG), group i / 8 % NG.
-  static constexpr int MW = (NG + 1) / 2;
+  // Pairs of tokens whose value scale and bias a lane converts a unit: word i = lane + 32 k of the
+  // unit's kMW, of granule i / (8 NG), group i / 8 % NG.
+  static constexpr int kMW = 8 * NG * UG, MW = (kMW + 31) / 32;
   // One warp's state of the current piece.
   struct State {
     float acc[VB * MPB][NT][4];
@@ -303,7 +320,7 @@ struct Kernel {
     float fs[MW], fb[MW];         // 2^(BITS - E), 2^-E of the groups this lane converts (convert_meta),
     uint32_t lim_s[MW], lim_b[MW];   // and the largest scale and |bias| (bf16 bits, in both halves) that 2^E holds
   };
-  static constexpr int kMeta = 128 * NG;              // bytes of a warp's converted scales and biases
+  static constexpr int kMeta = 8 * kMW;              // bytes of a warp's converted scales and biases
   static constexpr int kQ = GHP * D * 2;              // bytes of a piece's queries
   static __device__ __forceinline__ int meta_group(int k) { return (((threadIdx.x & 31) + 32 * k) / 8) % NG; }
 
@@ -351,19 +368,19 @@ struct Kernel {
   // time.  The granules' MMA chains are independent and stand side by side (an
   // MMA's result takes 25 cycles, its issue slot 8).
   static __device__ __forceinline__ void scores(const unsigned char *sm, const uint32_t (&qf)[KM][NT][2],
-                                                const float (&qsum)[NG][NT][2], float (&sc)[2][NT][4]) {
+                                                const float (&qsum)[NG][NT][2], float (&sc)[UG][NT][4]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     constexpr int WG = GS * BITS / 128;             // words (of a lane's row) a group
     const unsigned char *meta = sm + 2 * L.code_bytes + r * NG * 4;
     const unsigned char *row = sm + (r * 4 + c) * L.VW * 4;
     constexpr int MV = NG < 4 ? NG : 4;             // groups of a meta load
-    float ga[2][NT][4];
-    uint32_t km[2][2][MV];
+    float ga[UG][NT][4];
+    uint32_t km[UG][2][MV];
 #pragma unroll
     for (int a = 0; a < L.NW / (4 * L.VW); a++) {
-      uint32_t w[2][2][4];                          // [granule][row r, r + 8][word]
+      uint32_t w[UG][2][4];                         // [granule][row r, r + 8][word]
 #pragma unroll
-      for (int h = 0; h < 2; h++)
+      for (int h = 0; h < UG; h++)
 #pragma unroll
         for (int k = 0; k < 2; k++) {
           const unsigned char *p = row + h * GB + (a * 16 + 8 * k) * 4 * L.VW * 4;
@@ -382,7 +399,7 @@ struct Kernel {
 #pragma unroll
           for (int k = 0; k < 2; k++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < UG; h++) {
               const uint32_t x0 = w[h][0][v] >> (8 * k), x1 = w[h][1][v] >> (8 * k);
               const uint32_t m0 = 0x000f000fu, m1 = 0x00f000f0u;
 #pragma unroll
@@ -394,7 +411,7 @@ struct Kernel {
             }
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
+          for (int h = 0; h < UG; h++) {
             const uint32_t x0 = w[h][0][v], x1 = w[h][1][v], m0 = 0x00ff00ffu;
 #pragma unroll
             for (int t = 0; t < NT; t++) {
@@ -407,7 +424,7 @@ struct Kernel {
         if (i % WG == WG - 1) {
           const int g = i / WG;
 #pragma unroll
-          for (int h = 0; h < 2; h++)
+          for (int h = 0; h < UG; h++)
 #pragma unroll
             for (int k = 0; k < 2; k++) {
               if (g % MV == 0) {
@@ -449,7 +466,7 @@ struct Kernel {
     for (int k = 0; k < MW; k++) {
       const int i = lane + 32 * k, h = i / (8 * NG), gp = i % (8 * NG);
       su[k] = bu[k] = 0;
-      if (NG > 1 || lane < 16) {
+      if (kMW % 32 == 0 || i < kMW) {
         const unsigned char *p = sm + h * GB + 2 * L.code_bytes + 64 * NG + gp * 4;
         su[k] = *reinterpret_cast<const uint32_t *>(p);
         bu[k] = *reinterpret_cast<const uint32_t *>(p + 32 * NG);
@@ -501,7 +518,7 @@ struct Kernel {
       const int i = lane + 32 * k, hg = i / 8, pair = i % 8;
       const float z = (float)(1 << (BITS - 1)) * s.fb[k];
       const float s0 = bf_lo(su[k]), s1 = bf_hi(su[k]);
-      if (NG > 1 || lane < 16) {
+      if (kMW % 32 == 0 || i < kMW) {
         const uint32_t b = pack_h2(fmaf(s0, z, bf_lo(bu[k]) * s.fb[k]), fmaf(s1, z, bf_hi(bu[k]) * s.fb[k]));
         *reinterpret_cast<uint2 *>(buf + hg * 64 + pair * 8) = make_uint2(b, pack_h2(s0 * s.fs[k], s1 * s.fs[k]));
       }
@@ -583,19 +600,19 @@ struct Kernel {
                                               const float (&qsum)[NG][NT][2], const float (&sf)[NT][2], State &s) {
     const int lane = threadIdx.x & 31, r = lane >> 2;
     const int t0 = 4 * (r / 2) + r % 2;             // tokens of rows r and r + 8: t0, t0 + 2
-    float sc[2][NT][4], y[2][NT][4];
+    float sc[UG][NT][4], y[UG][NT][4];
     scores(sm, qf, qsum, sc);
     // ---- running max: moved only when a P would pass 2^14
     auto exponents = [&]() {
 #pragma unroll
-      for (int h = 0; h < 2; h++)
+      for (int h = 0; h < UG; h++)
 #pragma unroll
         for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int j = 0; j < 4; j++) y[h][t][j] = fmaf(sc[h][t][j], sf[t][j & 1], -s.m10[t][j & 1]);
       if (lo > 0 || valid < kUnit)                  // the sequence's last unit, or a page is missing
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+        for (int h = 0; h < UG; h++)
 #pragma unroll
           for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -605,7 +622,7 @@ struct Kernel {
     exponents();
     float top = y[0][0][0];
 #pragma unroll
-    for (int h = 0; h < 2; h++)
+    for (int h = 0; h < UG; h++)
 #pragma unroll
       for (int t = 0; t < NT; t++) top = fmaxf(fmaxf(fmaxf(y[h][t][0], y[h][t][1]), fmaxf(y[h][t][2], y[h][t][3])), top);
     if (__any_sync(kFull, top > kLogPMax)) {
@@ -615,7 +632,7 @@ struct Kernel {
         for (int e = 0; e < 2; e++) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 2; h++)
+          for (int h = 0; h < UG; h++)
 #pragma unroll
             for (int k = 0; k < 2; k++)
               if (16 * h >= lo && 16 * h + t0 + 2 * k < valid) mx = fmaxf(mx, sc[h][t][e + 2 * k] * sf[t][e]);
@@ -636,9 +653,9 @@ struct Kernel {
       exponents();
     }
     // ---- P, rounded to fp16 and transposed to the B operand: k = token, n = head
-    uint32_t ph[2][NT][2], pl[2][NT][2];
+    uint32_t ph[UG][NT][2], pl[UG][NT][2];
 #pragma unroll
-    for (int h = 0; h < 2; h++)
+    for (int h = 0; h < UG; h++)
 #pragma unroll
       for (int t = 0; t < NT; t++) {
         float p[4];
@@ -658,8 +675,8 @@ struct Kernel {
         }
       }
     convert_meta(sm, meta, s);
-    values(sm, meta, ph[0], pl[0], s);
-    values(sm + GB, meta + 64 * NG, ph[1], pl[1], s);
+#pragma unroll
+    for (int h = 0; h < UG; h++) values(sm + h * GB, meta + h * 64 * NG, ph[h], pl[h], s);
   }
 
   // Writes this warp's sums (value units, over 2^kLogP) and max / total to the join buffer.
@@ -733,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   float *join_ml = join + kWarps * K::GHP * K::SROW;
   unsigned char *meta = smem_raw + K::kJoin + warp * K::kMeta;
   unsigned char *qcta = smem_raw + K::kJoin + kWarps * K::kMeta;             // queries of a piece
-  unsigned char *ring = qcta + K::kQ + warp * a.depth * 2 * K::GB;
+  unsigned char *ring = qcta + K::kQ + warp * a.depth * K::kSlot;
   uint64_t *bar = bars + warp * 8;
 
   if (lane == 0)
@@ -756,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     const int HC = a.H * a.chunks, pair = alone ? blockIdx.x * kWarps + warp : blockIdx.x;
     st.b = pair / HC;
     st.hc = pair % HC;
-    if (st.b < a.B) st.left = places(units(tokens(a, st.b, st.hc == 0)));
+    if (st.b < a.B) st.left = places(units(a, tokens(a, st.b, st.hc == 0)));
     pair_sync();
   }                              // (the barriers also publish the mbarriers)
 
@@ -781,7 +798,11 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   }
   cursor_open<K::GB>(a, cp, st.u, way);
   cursor_settle<K::GB>(a, cp, way);
-  if (tid == 0 && a.mode == kCut) recs[blockIdx.x] = Rec{pc.b, pc.hc, pc.g, pc.n};
+  if (tid == 0 && a.mode == kCut) {
+    // this share begins behind the pair's first unit, and the share in front with that unit or before it
+    const bool cut = pc.g > 0 && st.u - st.per <= kPieceCost;
+    recs[blockIdx.x] = Rec{pc.b, pc.hc, cut ? 1 + (int)((pc.n + kPieceCost - st.u + st.per - 1) / st.per) : 0, 0};
+  }
 
   // The ring: units go in and out in order, slot after slot.  A slot's barrier completes a phase for every
   // unit, also for one without a copy, so that one parity serves all slots of a round.
@@ -792,23 +813,22 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   const uint32_t page_gran = (uint32_t)a.H << a.gshift;     // granules of a page
   auto issue = [&]() {                // the cursor's unit into slot_in
     if (cp.g >= cp.end) return;
-    // the second granule only where a token of it is in front of the length (its page may not exist)
-    const bool two = cp.g * kUnit + kv::kTok < cp.len;
-    unsigned char *dst = ring + slot_in * (2 * K::GB);
+    const bool two = cursor_two(a, cp);
+    unsigned char *dst = ring + slot_in * K::kSlot;
     uint64_t *full = bar + slot_in;
     // granule of the cache
     auto gran = [&](int page) {
-      return a.cache + ((int64_t)page * page_gran + (cp.head + (cp.g * 2 & ((1 << a.gshift) - 1)))) * K::GB;
+      return a.cache + ((int64_t)page * page_gran + (cp.head + ((cp.g << a.ushift) & ((1 << a.gshift) - 1)))) * K::GB;
     };
     if (max((uint32_t)cp.page0, (uint32_t)cp.page1) < (uint32_t)a.pages) {
       if (lane == 0) {
         const uint32_t bytes = two ? 2 * K::GB : K::GB;
         mbar_arrive_expect_tx(full, bytes);
-        if (a.gshift != 0) {                     // both in one page
+        if (a.gshift != 0 || !two) {             // all in one page
           bulk_load(dst, gran(cp.page0), bytes, full);
         } else {
           bulk_load(dst, gran(cp.page0), K::GB, full);
-          if (two) bulk_load(dst + K::GB, gran(cp.page1), K::GB, full);
+          bulk_load(dst + K::GB, gran(cp.page1), K::GB, full);
         }
       }
     } else {                                     // a granule whose page is outside the cache is left out and reported
@@ -936,17 +956,17 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
         break;
       }
       flying--;
-      unsigned char *sm = ring + slot_out * (2 * K::GB);
-      int lo = 0, valid = pc.len - g * kUnit;
-      if (valid < kUnit || (lack0 | lack1)) {        // a last unit, or one of few with a page outside the cache
+      unsigned char *sm = ring + slot_out * K::kSlot;
+      int lo = 0, valid = pc.len - g * K::kUnit;
+      if (valid < K::kUnit || (lack0 | lack1)) {        // a last unit, or one of few with a page outside the cache
         const uint32_t bit = 1u << slot_out;
         if (lack0 & bit) lo = kv::kTok;
-        if (lack1 & bit) valid = min(valid, kv::kTok);
+        if (K::UG == 1 || (lack1 & bit)) valid = min(valid, kv::kTok);
         lack0 &= ~bit;
         lack1 &= ~bit;
         if (lo < valid) {
           if (lo > 0 || valid < kv::kTok) K::clear_tail(sm, lo > 0 ? 0 : valid);
-          if (valid < kUnit) K::clear_tail(sm + K::GB, valid - kv::kTok);
+          if (K::UG == 2 && valid < K::kUnit) K::clear_tail(sm + K::GB, valid - kv::kTok);
         }
       }
       if (lo < valid) K::unit(sm, meta, lo, valid, qf, qsum, sf, s);
@@ -1026,109 +1046,89 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   }
 }
 
-// Joins the pieces of a pair that shares cut.  Block i looks at the boundary in
-// front of share i: if it is the first one inside its pair, the block adds the
-// piece that ends share i - 1 and those that begin share i, i + 1, ...: kJoinWarps
-// warps share the heads and, where they are more, a head's pieces; a lane takes
-// D / 32 elements.
-constexpr int kJoinWarps = 16;
+// Joins the pieces of the pairs that shares cut.  Block (i, h) reads the record of
+// share i + 1 and, where there is a pair to join, adds head h of the piece that
+// ends share i and of those that begin shares i + 1, i + 2, ...: the warps take
+// pieces in turn, a lane D / 32 elements, maxima, totals and sums loaded at once.
+constexpr int kJoinBatch = 8;
 
 template <int D, int GHP>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const Args a, int ctas) {
+__global__ void __launch_bounds__(kThreads) k_attn_join(const Args a, int ctas) {
   constexpr int kPart = Ws<D, GHP>::kPart, E = D / 32;
-  __shared__ float so[kJoinWarps][D], sml[kJoinWarps][2];
+  __shared__ float so[kWarps][D], sml[kWarps][2];
   pdl_launch_dependents();
   pdl_wait();
-  const Rec *recs = reinterpret_cast<const Rec *>(a.ws + (int64_t)2 * ctas * kPart);
-  const int i = blockIdx.x + 1;
+  const int i = blockIdx.x + 1, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (read through L2: nothing of the workspace may come from an earlier launch's lines in L1)
-  auto rec_at = [&](int j) {
-    const int4 v = __ldcg(reinterpret_cast<const int4 *>(recs + j));
-    return Rec{v.x, v.y, v.z, v.w};
-  };
-  const Rec rec = rec_at(i), prev = rec_at(i - 1);
-  if (rec.n == 0 || rec.g0 == 0) return;
-  if (prev.b == rec.b && prev.hc == rec.hc && prev.g0 > 0) return;   // an earlier boundary is inside this pair
-  const int chunk = rec.hc % a.chunks;
-  const int h0 = (rec.hc / a.chunks) * a.G + chunk * a.GH;
-  const int heads = min(a.GH, a.G - chunk * a.GH);
-  int last = i;                                                      // shares that begin inside the pair
-  for (bool more = true; more;) {
-    const int j = last + 1 + lane;
-    Rec nx{0, 0, 0, 0};
-    if (j < ctas) nx = rec_at(j);
-    const unsigned in = __ballot_sync(kFull, nx.n != 0 && nx.b == rec.b && nx.hc == rec.hc && nx.g0 > 0);
-    const int got = in == kFull ? 32 : __ffs(~in) - 1;
-    last += got;
-    more = got == 32;
-  }
+  const int4 rec = __ldcg(reinterpret_cast<const int4 *>(a.ws + (int64_t)2 * ctas * kPart) + i);
+  const int b = rec.x, chunk = rec.y % a.chunks, pieces = rec.z;
+  const int h0 = (rec.y / a.chunks) * a.G + chunk * a.GH;
+  if (pieces == 0 || h >= a.G - chunk * a.GH) return;
   // piece j = 0: end of share i - 1; j > 0: beginning of share i + j - 1
   auto part = [&](int j) { return a.ws + (int64_t)(j == 0 ? 2 * (i - 1) + 1 : 2 * (i + j - 1)) * kPart; };
-  const int pieces = last - i + 2;
-  int per = 1;                                                       // warps of a head
-  while (per * 2 * heads <= kJoinWarps) per *= 2;
-  const int h = warp / per, w = warp % per;
-  if (h < heads) {
-    // the common max first (lanes look at 32 pieces at once), so that the sums' loads do not wait for one another
-    auto ml_at = [&](int j) { return __ldcg(reinterpret_cast<const float2 *>(part(j) + GHP * D + 2 * h)); };
-    float m = -INFINITY, l = 0.0f, o[E];
-    for (int j = w + lane * per; j < pieces; j += 32 * per) {
-      const float2 ml = ml_at(j);
-      if (ml.y != 0.0f) m = fmaxf(m, ml.x);                          // (a piece without a token adds nothing)
-    }
+  float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+  for (int e = 0; e < E; e++) o[e] = 0.0f;
+  for (int j0 = warp; j0 < pieces; j0 += kWarps * kJoinBatch) {
+    float2 ml[kJoinBatch], v[kJoinBatch][E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e++) o[e] = 0.0f;
-    for (int j0 = w; j0 < pieces; j0 += 32 * per) {
-      float f = 0.0f, lj = 0.0f;                                     // of piece j0 + lane * per
-      if (j0 + lane * per < pieces) {
-        const float2 ml = ml_at(j0 + lane * per);
-        lj = ml.y;
-        f = lj == 0.0f ? 0.0f : ex2(ml.x - m);
+    for (int k = 0; k < kJoinBatch; k++) {
+      const int j = j0 + k * kWarps;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      if (j < pieces) {
+        const float *p = part(j);
+        ml[k] = __ldcg(reinterpret_cast<const float2 *>(p + GHP * D + 2 * h));
+#pragma unroll
+        for (int e = 0; e < E / 2; e++) v[k][e] = __ldcg(reinterpret_cast<const float2 *>(p + h * D + lane * E) + e);
       }
-      l = fmaf(lj, f, l);
-      const int n = min(32, (pieces - j0 + per - 1) / per);
-#pragma unroll 8
-      for (int k = 0; k < n; k++) {
-        const float *p = part(j0 + k * per) + h * D + lane * E;
-        const float fk = __shfl_sync(kFull, f, k);
+    }
+    float mn = m;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2 *>(p + e));
-          o[e] = fmaf(v.x, fk, o[e]);
-          o[e + 1] = fmaf(v.y, fk, o[e + 1]);
+    for (int k = 0; k < kJoinBatch; k++)
+      if (ml[k].y != 0.0f) mn = fmaxf(mn, ml[k].x);                  // (a piece without a token adds nothing)
+    const float fo = m == -INFINITY ? 0.0f : ex2(m - mn);
+    m = mn;
+    l *= fo;
+#pragma unroll
+    for (int e = 0; e < E; e++) o[e] *= fo;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; k++)
+      if (ml[k].y != 0.0f) {
+        const float f = ex2(ml[k].x - m);
+        l = fmaf(ml[k].y, f, l);
+#pragma unroll
+        for (int e = 0; e < E / 2; e++) {
+          o[2 * e] = fmaf(v[k][e].x, f, o[2 * e]);
+          o[2 * e + 1] = fmaf(v[k][e].y, f, o[2 * e + 1]);
         }
       }
-    }
+  }
 #pragma unroll
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
-#pragma unroll
-    for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
-    if (lane == 0) {
-      sml[warp][0] = m;
-      sml[warp][1] = l;
-    }
+  for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    sml[warp][0] = m;
+    sml[warp][1] = l;
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < heads * (D / 2); x += kJoinWarps * 32) {
-    const int hh = x / (D / 2), d = x % (D / 2) * 2;
-    float mt = -INFINITY, lt = 0.0f, x0 = 0.0f, x1 = 0.0f;
-    for (int k = hh * per; k < (hh + 1) * per; k++)
-      if (sml[k][1] != 0.0f) mt = fmaxf(mt, sml[k][0]);
-    for (int k = hh * per; k < (hh + 1) * per; k++) {
-      if (sml[k][1] == 0.0f) continue;
-      const float f = ex2(sml[k][0] - mt);
-      lt = fmaf(sml[k][1], f, lt);
-      x0 = fmaf(so[k][d], f, x0);
-      x1 = fmaf(so[k][d + 1], f, x1);
-    }
-    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-    const int64_t row = (int64_t)rec.b * a.H * a.G + h0 + hh;
-    store_out2(a, row * D + d, x0 * inv, x1 * inv);
-    if (a.lse && d == 0) a.lse[row] = lse_of(mt, lt);
+  if (threadIdx.x * 2 >= D) return;
+  const int d = threadIdx.x * 2;
+  float mt = -INFINITY, lt = 0.0f, x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++)
+    if (sml[w][1] != 0.0f) mt = fmaxf(mt, sml[w][0]);
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    if (sml[w][1] == 0.0f) continue;
+    const float f = ex2(sml[w][0] - mt);
+    lt = fmaf(sml[w][1], f, lt);
+    x0 = fmaf(so[w][d], f, x0);
+    x1 = fmaf(so[w][d + 1], f, x1);
   }
+  const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+  const int64_t row = (int64_t)b * a.H * a.G + h0 + h;
+  store_out2(a, row * D + d, x0 * inv, x1 * inv);
+  if (a.lse && d == 0) a.lse[row] = lse_of(mt, lt);
 }
 
 }  // namespace attn
@@ -1183,7 +1183,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   constexpr size_t join = K::kJoin + attn::kWarps * K::kMeta + K::kQ;   // (all multiples of 16)
   // ring depth: what lets the CTAs that the registers allow share an SM (227 KB less 1 KB a CTA and the
   // kernel's static part), at least 2 slots, at most 6
-  constexpr size_t slot = (size_t)attn::kWarps * 2 * K::GB, most = 227 * 1024 / attn::min_ctas(D, NT) - 1536;
+  constexpr size_t slot = (size_t)attn::kWarps * K::kSlot, most = 227 * 1024 / attn::min_ctas(D, NT) - 1536;
   int depth = join < most ? (int)((most - join) / slot) : 0;
   depth = depth < 2 ? 2 : (depth > 6 ? 6 : depth);
   const size_t smem = join + depth * slot;
@@ -1195,6 +1195,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   if (ws_bytes < need)
     return fail(GWB_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
   a.depth = depth;
+  a.ushift = K::UG - 1;
   const int64_t pairs = (int64_t)a.B * a.H * a.chunks;
   a.mode = attn_mode(pairs, a.cap, ctas);
   cudaLaunchConfig_t cfg = {};
@@ -1210,8 +1211,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
   if (a.mode != attn::kCut) return GWB_OK;
-  cfg.gridDim = dim3((unsigned)(ctas - 1));
-  cfg.blockDim = dim3(attn::kJoinWarps * 32);
+  cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)a.GH);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, attn::k_attn_join<D, K::GHP>, a, ctas);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode join launch: %s", cudaGetErrorString(e));
