@@ -777,14 +777,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     pair_sync();
   }                              // (the barriers also publish the mbarriers)
 
-  // rows without a token: zeros, and minus infinity for the log-sum-exp
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (tokens(a, b, false) == 0) {
-      const int64_t row = (int64_t)b * a.H * a.G;
-      for (int i = tid; i < a.H * a.G * D; i += kThreads) a.out[row * D + i] = 0;
-      if (a.lse)
-        for (int i = tid; i < a.H * a.G; i += kThreads) a.lse[row + i] = -INFINITY;
-    }
+  // rows without a token: zeros, and minus infinity for the log-sum-exp (a warp a row, behind the CTA's share)
+  auto empty_rows = [&]() {
+    for (int b = blockIdx.x * kWarps + warp; b < a.B; b += gridDim.x * kWarps)
+      if (tokens(a, b, false) == 0) {
+        const int64_t row = (int64_t)b * a.H * a.G;
+        for (int i = lane; i < a.H * a.G * (D / 8); i += 32) reinterpret_cast<uint4 *>(a.out + row * D)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (int i = lane; i < a.H * a.G; i += 32) a.lse[row + i] = -INFINITY;
+      }
+  };
   constexpr int kPart = Ws<D, K::GHP>::kPart;
   Rec *recs = reinterpret_cast<Rec *>(a.ws + (int64_t)2 * gridDim.x * kPart);
   // pieces walked by the whole CTA (pc), and this warp's copies (cp), ahead of it
@@ -794,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   cp.left = pc.left = st.left;
   if (!cursor_open<K::GB, false>(a, pc, st.u, 0)) {
     if (tid == 0 && a.mode == kCut) recs[blockIdx.x] = Rec{0, 0, 0, 0};
+    empty_rows();
     return;
   }
   cursor_open<K::GB>(a, cp, st.u, way);
@@ -1036,6 +1039,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
     first_piece = false;
     g_first = 0;
   }
+  empty_rows();
   // copies still in flight (only after a wait gave up) land before the CTA's memory is freed
   for (; flying > 0; flying--) {
     mbar_wait(bar + slot_out, parity);
