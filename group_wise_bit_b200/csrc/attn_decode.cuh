@@ -30,9 +30,21 @@
 // the unpacked registers takes four.  With PREC the codes do go through 1024 + code
 // and a subtraction instead, which makes them normal numbers and the products exact.
 //
+// What bounds it.  8-bit caches: memory (64 sequences of up to 8192 tokens, 8 kv
+// heads x 128, 64 query heads: 132 us = 6.1 TB/s, 0.93 of a plain copy).  4-bit
+// caches: the SM's work a token (the same at 4 bits: 101 us = 4.2 TB/s): about 285
+// issue slots a granule, 80 of them masks and shifts of codes, 25 MMAs; the copies
+// alone would take 80 us of 104 at 8 sequences of 65536 tokens.  Short calls: the
+// chain lengths, page ids, codes, queries, join (1 sequence of 128 tokens: 5 us).
+// Slower, and left out: e4m3 MMAs for the keys (a nibble is an e4m3 number; 131
+// against 112 us, with more instructions and fp16 MMAs counted, not fewer), a
+// granule's values beside the next one's scores (117), four CTAs an SM (115), the
+// shifts as multiplications (121), shares half or a third as long (118, 124).
+//
 // Precision.  q is scaled by a power of two per head into fp16 (exact for bf16
 // and fp16 but for elements 2^-27 below the largest).  Scores, maxima, totals
-// and outputs are fp32.  p is rounded to fp16 (2^-11) before it meets the codes,
+// and outputs are fp32; a score's MMA truncates at 2^-14 of a code step of its
+// largest |q|, well below what fp16 does to p.  p is rounded to fp16 (2^-11) before it meets the codes,
 // and p * sv again; with PREC (fp16 outputs, whose own rounding is no coarser)
 // the remainders of both roundings go through a second MMA.  Value scales and
 // biases are normalized by a running power of two a group, so fp16's range

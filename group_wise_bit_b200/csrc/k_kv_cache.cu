@@ -10,7 +10,10 @@
 //
 // Where a block's 16 slots are one granule, as in a prompt, its codes and metadata
 // go through shared memory in the cache's order and move in 16-byte pieces; else
-// every thread moves its own 2- and 4-byte units.
+// every thread moves its own 2- and 4-byte units.  8192 tokens of 8 heads x 128 at
+// 8 bits: write 17 us, read 12 us, against 8 us each for their 51 MB; the issue
+// slots bound both (the write's min, max, quotient and rounding are 23 operations
+// an element; it took 34 us with 8 elements a thread and 2-byte stores).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -6,7 +6,8 @@
  * ---------------------------------------
  *  - All tensor pointers are DEVICE pointers owned by the caller; the library
  *    never allocates, frees or retains them.  Tensors are dense and row-major
- *    with the shapes stated per call; no strides are taken.
+ *    with the shapes stated per call; no strides are taken but those that the
+ *    cache and attention calls name.
  *  - The library owns two kinds of device buffer.  The first is the persistent
  *    tensor-core GEMM's stream-K workspace (partial tiles, up to about 19 MB):
  *    one per (device, stream), allocated by the first call on that stream that
@@ -24,8 +25,9 @@
  *    validates its arguments synchronously, on the host, before launching
  *    anything; on success the work is enqueued on `stream` and the call returns
  *    without synchronizing.  A call that returns an error has launched nothing.
- *  - Pointers must be 16-byte aligned (GWB_ERR_ALIGN otherwise); optional
- *    pointers that may be NULL say so.
+ *  - Pointers must be 16-byte aligned (GWB_ERR_ALIGN otherwise; slots, page ids,
+ *    lengths and log-sum-exps need their own size only); optional pointers that
+ *    may be NULL say so.
  *  - The return value is a gwb_status; gwb_last_error() gives a readable
  *    message for the calling thread's most recent failure.
  *  - Device-side waits inside the tensor-core kernels are bounded; a wait that
@@ -51,7 +53,10 @@
  * module doc "Layout" and the Hugging Face transformers "Metal" quantization
  * page; "GPTQ" = TinyGPT "Quantization Expansion", section 1 "GPTQReader",
  * "Format" and dequant recipe; "QAT" = the same page, section 4, "Fake-quant +
- * STE"; "W4A8" = executorch PR #24467 "mlx::int8_int4_gemm".
+ * STE"; "W4A8" = executorch PR #24467 "mlx::int8_int4_gemm".  The norm, the
+ * quantized cache and the decode attention stand between a decoder's linear
+ * layers; the pages describe no kernel of theirs (the cache's quantizer is the
+ * MLX affine scheme).
  */
 #ifndef GWB_H
 #define GWB_H
