@@ -49,7 +49,7 @@ SIGNATURES = {
     "gwb_kv_block_bytes": [_I64, _INT, _INT, _INT, _P],
     "gwb_kv_write": [_P, _I64, _P, _I64, _P, _I64, _INT, _P, _I64, _I64, _I64, _INT, _INT, _INT, _P],
     "gwb_kv_read": [_P, _I64, _I64, _I64, _INT, _INT, _INT, _P, _I64, _INT, _P, _P, _P],
-    "gwb_attn_decode_workspace": [_I64, _I64, _INT, _P],
+    "gwb_attn_decode_workspace": [_I64, _I64, _INT, _I64, _I64, _P],
     "gwb_attn_decode": [_P, _I64, _I64, _I64, _INT, _P, _I64, _I64, _I64, _INT, _INT, _INT, _P, _I64, _I64, _P, _F32,
                         _P, _P, _P, _I64, _P],
     "gwb_check_device_error": [_P],
@@ -516,14 +516,17 @@ def kv_read(cache, slots, head_dim, bits, group_size, dtype=torch.bfloat16, k=No
 _ws_bytes = {}
 
 
-def attn_decode_workspace(q_heads, heads, head_dim):
-    """Bytes of attn_decode's workspace on the current device."""
-    key = (torch.cuda.current_device(), q_heads, heads, head_dim)
+def attn_decode_workspace(q_heads, heads, head_dim, batch=0, max_tokens=0):
+    """Bytes of attn_decode's workspace on the current device, for up to `batch` sequences whose page tables
+    name max_tokens tokens (0: any); none where the tables are short."""
+    key = (torch.cuda.current_device(), q_heads, heads, head_dim, batch, max_tokens)
     n = _ws_bytes.get(key)
     if n is None:
         out = _I64(0)
-        _call("gwb_attn_decode_workspace", q_heads, heads, head_dim, ctypes.byref(out))
-        n = _ws_bytes[key] = out.value
+        _call("gwb_attn_decode_workspace", q_heads, heads, head_dim, batch, max_tokens, ctypes.byref(out))
+        n = out.value
+        if len(_ws_bytes) < 4096:
+            _ws_bytes[key] = n
     return n
 
 
@@ -554,15 +557,17 @@ def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, ou
     if lse is not None:
         _dev(lse, "lse", (torch.float32,), (B, HQ))
     stream = _stream_of(q, cache, page_table, seq_lens, out, lse, workspace)
-    need = _ws_bytes.get((q.get_device(), HQ, heads, D)) or attn_decode_workspace(HQ, heads, D)
-    if workspace is None:
-        workspace = cache.new_empty(need)
-    else:
+    if workspace is not None:
         _dev(workspace, "workspace", (torch.uint8,))
+        ws = workspace.numel()
+    else:
+        ws = attn_decode_workspace(HQ, heads, D, B, max_pages * page_size)
+        if ws:
+            workspace = cache.new_empty(ws)
     _call("gwb_attn_decode", _ptr(q), qs, B, HQ, _HALF[q.dtype], _ptr(cache), pages, heads, page_size, D, bits,
           group_size, _ptr(page_table), ts, max_pages, _ptr(seq_lens),
           float(1.0 / D ** 0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(workspace),
-          workspace.numel(), stream)
+          ws, stream)
     return out
 
 

@@ -590,11 +590,14 @@ gwb_status check_heads(int64_t q_heads, int64_t heads) {
 
 }  // namespace
 
-gwb_status gwb_attn_decode_workspace(int64_t q_heads, int64_t heads, int head_dim, int64_t *bytes) {
+gwb_status gwb_attn_decode_workspace(int64_t q_heads, int64_t heads, int head_dim, int64_t B, int64_t max_tokens,
+                                     int64_t *bytes) {
   if (!bytes) return fail(GWB_ERR_INVALID_ARG, "bytes must not be NULL");
+  if (B < 0 || max_tokens < 0)
+    return fail(GWB_ERR_INVALID_ARG, "negative size (B=%lld, max_tokens=%lld)", (long long)B, (long long)max_tokens);
   GWB_TRY(check_cache(0, heads, 16, head_dim, 8, 32));
   GWB_TRY(check_heads(q_heads, heads));
-  return gwb::attn_workspace_bytes(q_heads, heads, head_dim, bytes);
+  return gwb::attn_workspace_bytes(q_heads, heads, head_dim, B, max_tokens, bytes);
 }
 
 gwb_status gwb_attn_decode(const uint16_t *q, int64_t q_stride, int64_t B, int64_t q_heads, int dtype,
@@ -616,7 +619,8 @@ gwb_status gwb_attn_decode(const uint16_t *q, int64_t q_stride, int64_t B, int64
   GWB_TRY(check_rows(q, "q", q_stride, q_heads * head_dim));
   GWB_TRY(need_index(seq_lens, "seq_lens", 4));
   GWB_TRY(need(out, "out"));
-  GWB_TRY(need(workspace, "workspace"));
+  if (workspace_bytes < 0) return fail(GWB_ERR_INVALID_ARG, "negative workspace_bytes");
+  if (workspace && !aligned16(workspace)) return fail(GWB_ERR_ALIGN, "workspace is not 16-byte aligned");
   if (lse) GWB_TRY(need_index(lse, "lse", 4));
   if (pages > 0) GWB_TRY(need(cache, "cache"));
   if (max_pages > 0) GWB_TRY(need_index(page_table, "page_table", 4));
@@ -625,7 +629,7 @@ gwb_status gwb_attn_decode(const uint16_t *q, int64_t q_stride, int64_t B, int64
   c.cache = gwb::KvCache{const_cast<void *>(cache), pages, heads, page_size, head_dim, bits, group_size};
   c.table = page_table; c.table_stride = table_stride; c.max_pages = max_pages;
   c.lens = seq_lens; c.scale = scale; c.f16 = dtype == GWB_F16;
-  c.out = out; c.lse = lse; c.ws = workspace; c.ws_bytes = workspace_bytes;
+  c.out = out; c.lse = lse; c.ws = workspace; c.ws_bytes = workspace ? workspace_bytes : 0;
   return gwb::launch_attn_decode(c, as_stream(stream));
 }
 

@@ -43,11 +43,35 @@ gwb_status attn_setup(const void *kern, size_t smem, int threads, AttnSetup *out
 // (head_dim <= 128): the codes are unpacked once for both 8-head tiles.
 int attn_tiles(int64_t group, int head_dim) { return group > 8 && head_dim <= 128 ? 2 : 1; }
 
-gwb_status attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, int64_t *bytes) {
+// Short sequences are not cut (one launch, nothing to join): a pair goes to a CTA, or to a warp where the pairs
+// are so many that the SMs want more of them at once.  us for B sequences of tables of L tokens (lengths L/2 .. L,
+// 4 bits, head_dim 128, 8 kv heads; 444 CTAs resident), cut / a CTA a pair / a warp a pair:
+//   B = 1    L = 128    7.3   5.0   8.6     512   10.6   8.9  22.6     1024   10.9  13.8
+//   B = 64   L = 128   15.5  11.6  11.5     512   22.9  19.0  28.7     1024   29.3  27.7     2048   44.5  47.4
+//   B = 128  L = 256   24.8  21.8  19.4     512   31.5  28.5  32.2     2048   74.7  75.1
+//   B = 256  L = 128   30.1  28.4  19.3     512   58.8  51.0  45.0     1024   85.9  77.2  81.2     2048  142  127
+// A longer table may hold one sequence that keeps its CTA busy behind all others, so it is always cut.
+constexpr int64_t kAttnUncut = 512, kAttnPairs = 1 << 20;
+
+AttnMode attn_mode(int64_t pairs, int64_t cap, int ctas) {
+  if (pairs > kAttnPairs) return kAttnCut;
+  if (cap <= kAttnUncut && cap * ctas <= 128 * pairs) return kAttnWarpPair;
+  if (cap <= kAttnUncut || (cap <= 2048 && pairs >= 4 * (int64_t)ctas)) return kAttnCtaPair;
+  return kAttnCut;
+}
+
+gwb_status attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, int64_t B, int64_t max_tokens,
+                                int64_t *bytes) {
   int dev = 0, sms = 0;
   const gwb_status s = sm_count(&dev, &sms);
   if (s != GWB_OK) return s;
-  const int64_t heads = 8 * attn_tiles(q_heads / kv_heads, head_dim);
+  const int64_t group = q_heads / kv_heads, heads = 8 * attn_tiles(group, head_dim);
+  // uncut whatever the number of resident CTAs, and for fewer sequences too: the table's width alone decides
+  if (B > 0 && max_tokens > 0 && max_tokens <= kAttnUncut &&
+      B <= kAttnPairs / (kv_heads * ((group + heads - 1) / heads))) {
+    *bytes = 0;
+    return GWB_OK;
+  }
   // two partials (sums, max and total a head) and a 16-byte record a CTA
   *bytes = (int64_t)sms * kAttnMaxPerSm * (2 * 4 * heads * (head_dim + 2) + 16);
   return GWB_OK;

@@ -85,12 +85,9 @@ struct Args {
   int depth;                    // ring slots a warp
   int min_per;                  // least places of a share
   int f16;
-  int mode;                     // kCut, kCtaPair, kWarpPair
+  int mode;                     // AttnMode
   float scale_log2;             // softmax scale * log2 e
 };
-
-// How pairs are spread: cut into equal shares; a CTA a pair; a warp a pair (no pair is cut in the last two).
-enum { kCut = 0, kCtaPair = 1, kWarpPair = 2 };
 
 // One record a CTA, for the join: the pair that the boundary in front of its share cuts, where no
 // earlier boundary does.
@@ -771,14 +768,14 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   pdl_launch_dependents();
   pdl_wait();
   // warps that share a pair, this one's number among them, and their barrier
-  const bool alone = a.mode == kWarpPair;
+  const bool alone = a.mode == kAttnWarpPair;
   const int ways = alone ? 1 : kWarps, way = alone ? 0 : warp;
   auto pair_sync = [&]() {
     if (alone) __syncwarp();
     else __syncthreads();
   };
   Start st{};
-  if (a.mode == kCut) {
+  if (a.mode == kAttnCut) {
     find_start(a, &start, scan);
     st = start;
   } else {
@@ -807,13 +804,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
   cp.hc = pc.hc = st.hc;
   cp.left = pc.left = st.left;
   if (!cursor_open<K::GB, false>(a, pc, st.u, 0)) {
-    if (tid == 0 && a.mode == kCut) recs[blockIdx.x] = Rec{0, 0, 0, 0};
+    if (tid == 0 && a.mode == kAttnCut) recs[blockIdx.x] = Rec{0, 0, 0, 0};
     empty_rows();
     return;
   }
   cursor_open<K::GB>(a, cp, st.u, way);
   cursor_settle<K::GB>(a, cp, way);
-  if (tid == 0 && a.mode == kCut) {
+  if (tid == 0 && a.mode == kAttnCut) {
     // this share begins behind the pair's first unit, and the share in front with that unit or before it
     const bool cut = pc.g > 0 && st.u - st.per <= kPieceCost;
     recs[blockIdx.x] = Rec{pc.b, pc.hc, cut ? 1 + (int)((pc.n + kPieceCost - st.u + st.per - 1) / st.per) : 0, 0};
@@ -1176,21 +1173,6 @@ attn::Args attn_args(const AttnCall &c) {
   return a;
 }
 
-// Short sequences are not cut (one launch, nothing to join): a pair goes to a CTA, or to a warp where the pairs
-// are so many that the SMs want more of them at once.  us for B sequences of tables of L tokens (lengths L/2 .. L,
-// 4 bits, head_dim 128, 8 kv heads; 444 CTAs resident), cut / a CTA a pair / a warp a pair:
-//   B = 1    L = 128    7.3   5.0   8.6     512   10.6   8.9  22.6     1024   10.9  13.8
-//   B = 64   L = 128   15.5  11.6  11.5     512   22.9  19.0  28.7     1024   29.3  27.7     2048   44.5  47.4
-//   B = 128  L = 256   24.8  21.8  19.4     512   31.5  28.5  32.2     2048   74.7  75.1
-//   B = 256  L = 128   30.1  28.4  19.3     512   58.8  51.0  45.0     1024   85.9  77.2  81.2     2048  142  127
-// A longer table may hold one sequence that keeps its CTA busy behind all others, so it is always cut.
-inline int attn_mode(int64_t pairs, int64_t cap, int ctas) {
-  if (pairs > 1 << 20) return attn::kCut;
-  if (cap <= 512 && cap * ctas <= 128 * pairs) return attn::kWarpPair;
-  if (cap <= 512 || (cap <= 2048 && pairs >= 4 * (int64_t)ctas)) return attn::kCtaPair;
-  return attn::kCut;
-}
-
 // Launches of one instance: the attention, then the join that depends on it.
 template <int BITS, int D, int GS, int NT, bool PREC>
 gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
@@ -1207,15 +1189,17 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   gwb_status s = attn_setup(reinterpret_cast<const void *>(kern), smem, attn::kThreads, &su);
   if (s != GWB_OK) return s;
   const int ctas = su.sms * (su.per_sm < kAttnMaxPerSm ? su.per_sm : kAttnMaxPerSm);
-  const int64_t need = (int64_t)ctas * (2 * 4 * attn::Ws<D, K::GHP>::kPart + (int64_t)sizeof(attn::Rec));
-  if (ws_bytes < need)
-    return fail(GWB_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
   a.depth = depth;
   a.ushift = K::UG - 1;
   const int64_t pairs = (int64_t)a.B * a.H * a.chunks;
   a.mode = attn_mode(pairs, a.cap, ctas);
+  const int64_t need = a.mode != kAttnCut
+                           ? 0
+                           : (int64_t)ctas * (2 * 4 * attn::Ws<D, K::GHP>::kPart + (int64_t)sizeof(attn::Rec));
+  if (ws_bytes < need)
+    return fail(GWB_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.mode == attn::kCut ? ctas : a.mode == attn::kCtaPair ? pairs : (pairs + attn::kWarps - 1) / attn::kWarps));
+  cfg.gridDim = dim3((unsigned)(a.mode == kAttnCut ? ctas : a.mode == kAttnCtaPair ? pairs : (pairs + attn::kWarps - 1) / attn::kWarps));
   cfg.blockDim = dim3(attn::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -1226,7 +1210,7 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode launch: %s", cudaGetErrorString(e));
-  if (a.mode != attn::kCut) return GWB_OK;
+  if (a.mode != kAttnCut) return GWB_OK;
   cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)a.GH);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, attn::k_attn_join<D, K::GHP>, a, ctas);

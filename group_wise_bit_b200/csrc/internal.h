@@ -79,7 +79,12 @@ struct AttnSetup {
 };
 gwb_status attn_setup(const void *kern, size_t smem, int threads, AttnSetup *out);
 int attn_tiles(int64_t group, int head_dim);
-gwb_status attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, int64_t *bytes);
+gwb_status attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, int64_t B, int64_t max_tokens,
+                                int64_t *bytes);
+// How pairs (sequence, chunk of a kv head's query heads) are spread: cut into equal shares, a CTA a pair, a warp
+// a pair (attn_decode.cu has the rule).
+enum AttnMode { kAttnCut = 0, kAttnCtaPair = 1, kAttnWarpPair = 2 };
+AttnMode attn_mode(int64_t pairs, int64_t cap, int ctas);
 gwb_status launch_attn_decode(AttnCall c, cudaStream_t st);
 gwb_status launch_attn_4_bf16(const AttnCall &c, cudaStream_t st);
 gwb_status launch_attn_4_fp16(const AttnCall &c, cudaStream_t st);

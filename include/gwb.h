@@ -420,15 +420,19 @@ gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t 
  *   seq_lens    int32 [B]; 0 (or less) is an empty row: zeros, lse = -inf
  *   out         [B, q_heads, head_dim], dense, of q's dtype
  *   lse         fp32 [B, q_heads] or NULL: log of sum_t p[t] (natural logarithm)
- *   workspace   gwb_attn_decode_workspace() bytes, contents irrelevant before and after; calls that
- *               may overlap on the GPU need one each
+ *   workspace   gwb_attn_decode_workspace() bytes (NULL where that is none), contents irrelevant before
+ *               and after; calls that may overlap on the GPU need one each
  * Lengths are read on the device only, so a captured graph follows them.  A
  * length beyond max_pages * page_size is cut to it, and the 16 tokens of a
  * granule whose page id is outside the cache are left out; both are reported
  * by gwb_check_device_error.  Scores, sums and the softmax are fp32; keys, values
  * and q enter exactly, the softmax weights as fp16 (with bf16 outputs) or as
  * fp16 pairs (with fp16 outputs).  Deterministic for given lengths and device. */
-gwb_status gwb_attn_decode_workspace(int64_t q_heads, int64_t heads, int head_dim, int64_t *bytes);
+/* Bytes of the workspace on the current device for at most B sequences (0: any number) whose page
+ * tables name max_tokens tokens (max_pages * page_size; 0: any): none where such calls cut no sequence,
+ * and then `workspace` may be NULL. */
+gwb_status gwb_attn_decode_workspace(int64_t q_heads, int64_t heads, int head_dim, int64_t B,
+                                     int64_t max_tokens, int64_t *bytes);
 gwb_status gwb_attn_decode(const uint16_t *q, int64_t q_stride, int64_t B, int64_t q_heads, int dtype,
                            const void *cache, int64_t pages, int64_t heads, int64_t page_size,
                            int head_dim, int bits, int group_size, const int32_t *page_table,

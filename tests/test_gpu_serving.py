@@ -276,8 +276,11 @@ def test_binding_refusals_on_the_gpu():
                      k, 4, 32)
     q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
     table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    long = torch.zeros(2, 64, dtype=torch.int32, device=DEV)          # 1024 tokens: such tables are cut
     with pytest.raises(gwb.GwbError, match="workspace"):
-        gwb.attn_decode(q, cache, table, lens, 4, 32, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+        gwb.attn_decode(q, cache, long, lens, 4, 32, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    assert gwb.attn_decode_workspace(4, 2, 64, 2, 512) == 0
+    assert 0 < gwb.attn_decode_workspace(4, 2, 64, 2, 1024) == gwb.attn_decode_workspace(4, 2, 64)
     with pytest.raises(gwb.GwbError, match="SHAPE"):
         gwb.attn_decode(q[:, :3].contiguous(), cache, table, lens, 4, 32)
     with pytest.raises(TypeError, match="page_table"):

@@ -108,8 +108,9 @@ def test_attention_refusals():
     assert call(ts=3) == 2
     assert call(dt=3) == 3
     assert call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
-    for name in ("q", "cache", "table", "lens", "out", "ws"):
+    for name in ("q", "cache", "table", "lens", "out"):
         assert call(**{name: NULL}) == 1, name
+    assert call(n=-1) == 1
     for name in ("q", "cache", "out", "ws"):
         assert call(**{name: OK8}) == 4, name
     for name in ("table", "lens", "lse"):
@@ -131,8 +132,9 @@ def test_block_bytes():
                     assert st == 0 and n.value == 64 * 2 * (D * bits // 8 + D // gs * 4)
                     assert n.value == 4 * S.Layout(bits, D, gs).bytes
     assert _st("gwb_kv_block_bytes", 64, 128, 4, 64, NULL) == 1
-    assert _st("gwb_attn_decode_workspace", 8, 3, 128, ctypes.byref(n)) == 2
-    assert _st("gwb_attn_decode_workspace", 8, 2, 128, NULL) == 1
+    assert _st("gwb_attn_decode_workspace", 8, 3, 128, 0, 0, ctypes.byref(n)) == 2
+    assert _st("gwb_attn_decode_workspace", 8, 2, 128, 0, 0, NULL) == 1
+    assert _st("gwb_attn_decode_workspace", 8, 2, 128, -1, 0, ctypes.byref(n)) == 1
 
 
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
