@@ -129,18 +129,18 @@ struct Part {
 template <int BITS, int LG>
 __device__ __forceinline__ void quantize(const float (&v)[kE], uint32_t (&words)[kE * BITS / 32], float &s, float &mn) {
   constexpr float QMAX = (float)((1 << BITS) - 1);
-  // (min and max order -0 below +0, as qpack_affine's keys do)
-  float mx = v[0];
-  mn = v[0];
+  // (min and max order -0 below +0, as qpack_affine's keys do; a NaN makes scale and bias NaN, its codes 0)
+  float mx = max_nan(v[0], v[1]);
+  mn = min_nan(v[0], v[1]);
 #pragma unroll
-  for (int j = 1; j < kE; j++) {
-    mn = fminf(mn, v[j]);
-    mx = fmaxf(mx, v[j]);
+  for (int j = 2; j < kE; j += 2) {
+    mn = min_nan(mn, v[j], v[j + 1]);
+    mx = max_nan(mx, v[j], v[j + 1]);
   }
 #pragma unroll
   for (int o = 1; o < LG; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(kFull, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    mn = min_nan(mn, __shfl_xor_sync(kFull, mn, o));
+    mx = max_nan(mx, __shfl_xor_sync(kFull, mx, o));
   }
   s = quotient_const<(1 << BITS) - 1>(__fsub_rn(mx, mn));
   const Divisor d = make_divisor(s);

@@ -39,9 +39,9 @@ __device__ __forceinline__ uint16_t from_f(float f) {
   else return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
-// The int8 code of y over a row's scale, by the division itself.
+// The int8 code of y over a row's scale, by the division itself; 0 for rows of zeros and rows that are not finite.
 __device__ __forceinline__ int quant_slow(float y, float s) {
-  return s == 0.0f ? 0 : (int)fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f);
+  return !(s > 0.0f && s < INFINITY) ? 0 : (int)fminf(fmaxf(rintf(__fdiv_rn(y, s)), -127.0f), 127.0f);
 }
 
 // Two values of 16 bits a word, as fp32.
@@ -68,7 +68,7 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(kFull, v, o));
   return v;
 }
 
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(V > 2 ? 512 : 1024) k_rmsnorm_row(const NormAr
       const float2 f = to_f2<F16>(h[i]), g = to_f2<F16>(w[i]);
       y[v][2 * i] = __fmul_rn(__fmul_rn(f.x, r), g.x);
       y[v][2 * i + 1] = __fmul_rn(__fmul_rn(f.y, r), g.y);
-      amax = fmaxf(fmaxf(fabsf(y[v][2 * i]), fabsf(y[v][2 * i + 1])), amax);
+      amax = max_nan(amax, fabsf(y[v][2 * i]), fabsf(y[v][2 * i + 1]));
     }
   }
   amax = block_max(amax, red_f);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_wide(const NormArgs a) {
   const float r = block_rstd(sum, red_d, &rstd_s, K, a.eps);
   float amax = 0.0f;
   for (int64_t i = threadIdx.x; i < K; i += blockDim.x)
-    amax = fmaxf(amax, fabsf(__fmul_rn(__fmul_rn(value(i, false), r), to_f<F16>(__ldg(a.weight + i)))));
+    amax = max_nan(amax, fabsf(__fmul_rn(__fmul_rn(value(i, false), r), to_f<F16>(__ldg(a.weight + i)))));
   amax = block_max(amax, red_f);
   const float s = __fdiv_rn(amax, 127.0f);
   if (threadIdx.x == 0) a.sx[m] = s;

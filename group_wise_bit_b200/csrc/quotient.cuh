@@ -1,5 +1,6 @@
-// Quotients of many numbers by one divisor, each rounded as the division itself
-// rounds it, and the nearest integer of such a quotient.
+// What the quantizers share: maxima that keep a NaN, quotients of many numbers by
+// one divisor, each rounded as the division itself rounds it, and the nearest
+// integer of such a quotient.
 //
 // With y = RN(1/b), q = RN(a y), the remainder r = a - q b is exact in one FMA
 // and RN(q + r y) is the correctly rounded a / b, unless b's significand is all
@@ -39,6 +40,24 @@ __device__ __forceinline__ float quotient_const(float a) {
   if (!(a >= 0x1p-90f && a <= 0x1p120f)) return __fdiv_rn(a, b);
   const float q = __fmul_rn(a, y);
   return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+}
+
+// Largest and smallest of two or three numbers; NaN where one is NaN (fmaxf and fminf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
+  return a;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  asm("min.NaN.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
+  return a;
 }
 
 // Round half to even of |x| <= 2^22 as the low bits of a float (two's complement from bit 0).

@@ -352,7 +352,9 @@ gwb_status gwb_gemm_i8i8(const int8_t *qx, const float *sx, int64_t M, const int
  *   sx[m] = max_k |y| / 127;  qx[m,k] = clip(round_half_even(y / sx[m]), -127, 127)
  * (0 when the row of y is zero).  The quantizer is gwb_quant_per_token_i8's, on
  * the fp32 norm instead of a rounded copy of it.
- *   x, residual  bf16 / fp16 [M, K] (finite; residual NULL or given together with residual_out)
+ * A row with a NaN or an infinity in h or y (a sum may overflow) has an sx that
+ * is not finite, and codes 0.
+ *   x, residual  bf16 / fp16 [M, K] (residual NULL or given together with residual_out)
  *   weight       bf16 / fp16 [K]
  *   residual_out [M, K] h, may be x or residual themselves
  *   qx int8 [M, K], sx fp32 [M]
@@ -393,7 +395,8 @@ gwb_status gwb_dequant_per_token_i8(const int8_t *qx, const float *sx, int64_t M
 gwb_status gwb_kv_block_bytes(int64_t page_size, int head_dim, int bits, int group_size, int64_t *bytes);
 
 /* kv_write -- quantizes T tokens' keys and values into their slots.
- *   k, v   [T, heads, head_dim] (finite), tokens k_stride / v_stride elements apart
+ *   k, v   [T, heads, head_dim], tokens k_stride / v_stride elements apart; a group
+ *          with a NaN or an infinity reads back as NaN
  *   slots  int64 [T] on the device; a negative slot is a padded row, which is
  *          left out, and so is one beyond the cache (see gwb_check_device_error).
  * Slots must be distinct: a slot named twice holds a mixture of its rows
@@ -427,7 +430,10 @@ gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t 
  * granule whose page id is outside the cache are left out; both are reported
  * by gwb_check_device_error.  Scores, sums and the softmax are fp32; keys, values
  * and q enter exactly, the softmax weights as fp16 (with bf16 outputs) or as
- * fp16 pairs (with fp16 outputs).  Deterministic for given lengths and device. */
+ * fp16 pairs (with fp16 outputs).  A key that is not finite makes the rows of its
+ * sequence and kv head NaN, a value its group of their columns; what lies behind
+ * a sequence's end or on pages that it does not name is never read into a sum.
+ * Deterministic for given lengths and device. */
 /* Bytes of the workspace on the current device for at most B sequences (0: any number) whose page
  * tables name max_tokens tokens (max_pages * page_size; 0: any): none where such calls cut no sequence,
  * and then `workspace` may be NULL. */

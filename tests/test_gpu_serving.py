@@ -79,6 +79,31 @@ def test_norm_edges(dt):
         _check_norm(tiny, None, S.bf16(w * 2.0 ** -130), dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K", [(5, 72), (5, 77), (700, 4096), (5, 40000)])
+def test_norm_rows_that_are_not_finite(M, K, dt):
+    """A NaN, an infinity, a sum that overflows: sx is not finite and the codes are 0; other rows keep their results."""
+    rng = np.random.default_rng(K)
+    x, r, w = _rand(rng, (M, K), dt), _rand(rng, (M, K), dt), S.rnd(1 + 0.1 * rng.standard_normal(K), dt == "fp16")
+    q_o, s_o, h_o = S.rmsnorm_quant_i8(x, r, w, 1e-5, dt == "fp16")
+    xt, rt = _t(x, dt), _t(r, dt)
+    xt[0, K - 1] = float("nan")
+    xt[2, 3] = float("-inf")
+    xt[3, 0] = rt[3, 0] = torch.finfo(DT[dt]).max
+    q, s, h = gwb.rmsnorm_quant_i8(xt, _t(w, dt), 1e-5, residual=rt)
+    bad = [0, 2, 3]
+    assert torch.isnan(s[bad]).all() and not q[bad].any()
+    assert torch.isnan(h[0, -1]) and h[2, 3] == float("-inf") and h[3, 0] == float("inf")
+    good = np.setdiff1d(np.arange(M), bad)
+    assert np.array_equal(q.cpu().numpy()[good], q_o[good]) and np.array_equal(s.cpu().numpy()[good], s_o[good])
+    assert np.array_equal(_np(h)[good], h_o[good])
+    # a weight that is not finite: every row
+    wt = _t(w, dt)
+    wt[K // 2] = float("nan")
+    q, s, _ = gwb.rmsnorm_quant_i8(_t(x, dt), wt, 1e-5)
+    assert torch.isnan(s).all() and not q.any()
+
+
 def test_norm_in_place_and_into_given_outputs():
     rng = np.random.default_rng(11)
     M, K = 6, 1000
@@ -154,6 +179,32 @@ def test_cache_write_and_read_bit_exact(bits, D, gs, dt):
             ref = (code * np.repeat(s, gs, -1) + np.repeat(b, gs, -1)).astype(np.float32)
             assert np.array_equal(_np(got), S.rnd(ref, out == "fp16"))
     gwb.check_device_error()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("bits,D,gs", LAYOUTS)
+def test_cache_groups_that_are_not_finite(bits, D, gs, dt):
+    """A group with a NaN or an infinity reads back as NaN; every other byte of the cache is what it was without."""
+    rng = np.random.default_rng(bits * D + gs)
+    T, H, page = 32, 2, 32
+    k, v = _t(_rand(rng, (T, H, D), dt), dt), _t(_rand(rng, (T, H, D), dt), dt)
+    for order in (torch.arange(T), torch.randperm(T)):          # whole granules, single rows
+        slots = order.to(DEV)
+        ref = gwb.kv_cache(1, H, D, page, bits, gs)
+        gwb.kv_write(ref, slots, k, v, bits, gs)
+        for what, x in enumerate((k, v)):
+            bad = x.clone()
+            hit = torch.zeros(T, H, D // gs, dtype=torch.bool, device=DEV)
+            for i, value in enumerate((float("nan"), float("inf"), float("-inf"))):
+                at = (5 * i + 1, i % H, (37 * i) % D)
+                bad[at] = value
+                hit[at[0], at[1], at[2] // gs] = True
+            cache = gwb.kv_cache(1, H, D, page, bits, gs)
+            gwb.kv_write(cache, slots, *((bad, v) if what == 0 else (k, bad)), bits, gs)
+            rows, clean = gwb.kv_read(cache, slots, D, bits, gs), gwb.kv_read(ref, slots, D, bits, gs)
+            cols = hit.repeat_interleave(gs, 2)
+            assert torch.isnan(rows[what][cols]).all()
+            assert torch.equal(rows[what][~cols], clean[what][~cols]) and torch.equal(rows[1 - what], clean[1 - what])
 
 
 def test_cache_rows_are_the_affine_packers():
@@ -437,6 +488,40 @@ def test_attention_values_far_outside_fp16():
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 0.01])
 def test_attention_scales(scale):
     Batch([200, 3], 2, 4, 64, 8, 64, 16, "bf16", seed=6).check(scale=scale)
+
+
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("lens,dt,bits", [([40, 700, 3], "bf16", 4), ([40, 700, 3], "fp16", 8), ([40, 300, 3], "bf16", 8)])
+def test_attention_rows_that_are_not_finite_stay_among_themselves(lens, dt, bits, value):
+    """In a sequence: a key makes its kv head's rows NaN, a value its group of columns.  Behind the end: nothing."""
+    H, G, D, gs = 2, 4, 128, 32
+    b = Batch(lens, H, G, D, bits, gs, 64, dt, seed=21)
+    good, good_lse = b.run()
+    k, v = _t(b.k, "bf16"), _t(b.v, "bf16")
+    for place in (0, lens[1] // 2, lens[1] - 1):
+        i = lens[0] + place                            # a token of sequence 1
+        bad = k[i:i + 1].clone()
+        bad[0, 1, 70] = float(value)
+        gwb.kv_write(b.cache, b.slots[i:i + 1], bad, v[i:i + 1], bits, gs)
+        out, lse = b.run()
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[1, G:] = True
+        assert torch.equal(torch.isnan(out), hit) and torch.equal(out[~hit], good[~hit])
+        assert torch.equal(torch.isnan(lse), hit[..., 0]) and torch.equal(lse[~hit[..., 0]], good_lse[~hit[..., 0]])
+        bad = v[i:i + 1].clone()
+        bad[0, 0, 33] = float(value)
+        gwb.kv_write(b.cache, b.slots[i:i + 1], k[i:i + 1], bad, bits, gs)
+        out, lse = b.run()
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[1, :G, gs:2 * gs] = True
+        assert torch.equal(torch.isnan(out), hit) and torch.equal(out[~hit], good[~hit]) and torch.equal(lse, good_lse)
+        gwb.kv_write(b.cache, b.slots[i:i + 1], k[i:i + 1], v[i:i + 1], bits, gs)
+    # the row behind a sequence's last, in its last page
+    slot = b.slots[lens[0] - 1:lens[0]] + 1
+    both = torch.full((1, H, D), float(value), dtype=torch.bfloat16, device=DEV)
+    gwb.kv_write(b.cache, slot, both, both, bits, gs)
+    out, lse = b.run()
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
 
 
 def test_attention_strided_queries_tables_and_given_workspace():
