@@ -2,6 +2,7 @@
 // device holds of it, and the workspace's size.
 #include <map>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include "internal.h"
@@ -33,7 +34,12 @@ gwb_status attn_setup(const void *kern, size_t smem, int threads, AttnSetup *out
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&s.per_sm, kern, threads, smem);
     if (e != cudaSuccess) return fail(GWB_ERR_CUDA, "attn_decode setup: %s", cudaGetErrorString(e));
     if (s.per_sm < 1) return fail(GWB_ERR_CUDA, "attn_decode: %zu bytes of shared memory do not fit", smem);
-    it = g_setup.emplace(std::make_pair(dev, kern), s).first;
+    *out = s;
+    try {
+      g_setup.emplace(std::make_pair(dev, kern), s);
+    } catch (const std::bad_alloc &) {               // looked up again by the next call
+    }
+    return GWB_OK;
   }
   *out = it->second;
   return GWB_OK;

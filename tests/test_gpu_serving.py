@@ -491,7 +491,8 @@ def test_attention_scales(scale):
 
 
 @pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
-@pytest.mark.parametrize("lens,dt,bits", [([40, 700, 3], "bf16", 4), ([40, 700, 3], "fp16", 8), ([40, 300, 3], "bf16", 8)])
+@pytest.mark.parametrize("lens,dt,bits", [([40, 700, 3], "bf16", 4), ([40, 700, 3], "fp16", 8), ([40, 300, 3], "bf16", 8),
+                                          ([40, 300, 3], "fp16", 4)])
 def test_attention_rows_that_are_not_finite_stay_among_themselves(lens, dt, bits, value):
     """In a sequence: a key makes its kv head's rows NaN, a value its group of columns.  Behind the end: nothing."""
     H, G, D, gs = 2, 4, 128, 32
