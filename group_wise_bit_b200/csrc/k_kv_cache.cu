@@ -11,7 +11,7 @@
 // Where a block's 16 slots are one granule, as in a prompt, its codes and metadata
 // go through shared memory in the cache's order and move in 16-byte pieces; else
 // every thread moves its own 2- and 4-byte units.  8192 tokens of 8 heads x 128 at
-// 8 bits: write 17 us, read 12 us, against 8 us each for their 51 MB; the issue
+// 8 bits: write 13.2 us, read 13.7 us, against 8 us each for their 51 MB; the issue
 // slots bound both (the write's min, max, quotient and rounding are 23 operations
 // an element; it took 34 us with 8 elements a thread and 2-byte stores).
 #include <cuda_bf16.h>
@@ -27,6 +27,11 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kE = 16;                    // elements of a thread
+// Threads of an SM that the registers are shared out for (64 and 56 a thread).  us at 8192 tokens of 8 x 128, 8 bits:
+// write 15.5 with the compiler's 80 registers, 13.9 with 64, 15.9 with 48; read of 20011 tokens of 4 x 64, 4 bits:
+// 10.0 with 64, 8.8 with 56 or 48, and of 3000 tokens of 32 x 128, 8 bits: 18.6 with 56, 23.2 with 48.
+constexpr int kWriteThreads = 1024, kReadThreads = 1152;
+constexpr int kBlockCost = 4;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -180,7 +185,7 @@ __device__ __forceinline__ void quantize(const float (&v)[kE], uint32_t (&words)
 }
 
 template <int BITS, int D, int GS, bool F16>
-__global__ void __launch_bounds__(D) k_kv_write(const KvArgs a) {
+__global__ void __launch_bounds__(D, kWriteThreads / D) k_kv_write(const KvArgs a) {
   using P = Part<BITS, D, GS>;
   constexpr int LG = GS / kE;             // threads of a group
   constexpr int W = kE * BITS / 32;       // words of a thread
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(D) k_kv_write(const KvArgs a) {
 }
 
 template <int BITS, int D, int GS, bool F16>
-__global__ void __launch_bounds__(D) k_kv_read(const KvArgs a) {
+__global__ void __launch_bounds__(D, kReadThreads / D) k_kv_read(const KvArgs a) {
   using P = Part<BITS, D, GS>;
   __shared__ __align__(16) unsigned char buf[2][P::kBytes];
   constexpr int kPer = (P::kBytes / 16 + D - 1) / D, W = kE * BITS / 32;
@@ -326,13 +331,28 @@ __global__ void __launch_bounds__(D) k_kv_read(const KvArgs a) {
   }
 }
 
+// Heads of a block: as many as make the whole launch shortest, where a block costs as much as two heads (its slots
+// and first rows have to arrive) and the resident blocks go in rounds.  us, write / read, against as many heads as
+// leave 8 blocks an SM: 4096 tokens of 2 x 256, 8 bits 7.3 / 7.2 -> 6.5 / 6.5; 3000 of 32 x 128 20.5 / 20.8 ->
+// 18.7 / 18.4; 20011 of 4 x 64, 4 bits 12.3 / 10.3 -> 11.1 / 9.8 (all with 64 registers); a block's cost of one
+// head instead of two: 32768 of 8 x 128 46.4 / 46.7, not 44.1 / 46.1.  Few tokens get one head a block.
+int heads_of_block(int64_t tiles, int H, int64_t resident) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int h = 1; h <= H && h <= 64; h++) {
+    const int64_t blocks = tiles * ((H + h - 1) / h), cost = (blocks + resident - 1) / resident * (2 * h + kBlockCost);
+    if (cost < least) {
+      least = cost;
+      best = h;
+    }
+  }
+  return best;
+}
+
 template <int BITS, int D, int GS>
 void launch(KvArgs a, bool f16, bool write, cudaStream_t st) {
-  // heads in turn only where the tokens alone fill the GPU: 8 blocks an SM
   const int64_t tiles = (a.T + kv::kTok - 1) / kv::kTok;
-  int64_t z = (148 * 8 + 2 * tiles - 1) / (2 * tiles);
-  z = z < 1 ? 1 : (z > a.H ? a.H : z);
-  a.heads = (int)((a.H + z - 1) / z);
+  a.heads = heads_of_block(2 * tiles, a.H, 148 * ((write ? kWriteThreads : kReadThreads) / D));
   const dim3 grid((unsigned)tiles, 2, (unsigned)((a.H + a.heads - 1) / a.heads));
   if (write) {
     if (f16) k_kv_write<BITS, D, GS, true><<<grid, D, 0, st>>>(a);
