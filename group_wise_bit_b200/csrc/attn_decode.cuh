@@ -45,10 +45,14 @@
 // and fp16 but for elements 2^-27 below the largest).  Scores, maxima, totals
 // and outputs are fp32; a score's MMA truncates at 2^-14 of a code step of its
 // largest |q|, well below what fp16 does to p.  p is rounded to fp16 (2^-11) before it meets the codes,
-// and p * sv again; with PREC (fp16 outputs, whose own rounding is no coarser)
-// the remainders of both roundings go through a second MMA.  Value scales and
+// p * sv again, and the centred bias bv + Z sv too: 2^-11 of each, against the
+// 2^-8 of a bf16 output.  With PREC (fp16 outputs, whose own rounding is 2^-11)
+// the remainders of all three roundings take part: p and p * sv through a second
+// MMA, the biases' in rows of their MMA that are free.  Value scales and
 // biases are normalized by a running power of two a group, so fp16's range
-// limits nothing but ratios inside one group's column.
+// limits nothing but ratios inside one group's column: a value below 2^-14 of
+// the largest that the column has met loses bits (fp16's subnormals), whatever
+// the larger one's weight.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -66,6 +70,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLogP = 10.0f;      // P = p * 2^10 in fp16
 constexpr float kLogPMax = 14.0f;   // a larger P moves the running max
+constexpr int kLogB = 11;           // the remainders of the biases are held times 2^kLogB
 
 struct Args {
   const uint16_t *q;
@@ -323,13 +328,15 @@ struct Kernel {
   // One warp's state of the current piece.
   struct State {
     float acc[VB * MPB][NT][4];
-    float bacc[NT][4];            // [0], [1] of row r < NG: sum of P * (bias + Z scale) of group r
+    // of row r < NG, group r: [0], [1] sum of P * (bias + Z scale), with PREC [2], [3] of P * 2^kLogB times what
+    // the rounding of those biases left
+    float bacc[NT][4];
     float m10[NT][2], l[NT][2];   // running max (log2, minus kLogP) and this lane's total, heads 8 nt + 2c, +1
     int E[NG];                    // value scales and biases are held over 2^E
     float fs[MW], fb[MW];         // 2^(BITS - E), 2^-E of the groups this lane converts (convert_meta),
     uint32_t lim_s[MW], lim_b[MW];   // and the largest scale and |bias| (bf16 bits, in both halves) that 2^E holds
   };
-  static constexpr int kMeta = 8 * kMW;              // bytes of a warp's converted scales and biases
+  static constexpr int kMeta = (PREC ? 12 : 8) * kMW;   // bytes of a warp's converted scales and biases
   static constexpr int kQ = GHP * D * 2;              // bytes of a piece's queries
   static __device__ __forceinline__ int meta_group(int k) { return (((threadIdx.x & 31) + 32 * k) / 8) % NG; }
 
@@ -466,6 +473,9 @@ struct Kernel {
   // The unit's value scales (over 2^(E - BITS)) and centred biases (bias + Z scale, over 2^E) as fp16, each
   // converted once into the warp's buffer: [granule][group][c][bias, scale of tokens 4c, 4c + 1; bias, scale of
   // 4c + 2, 4c + 3], an A operand as it stands: rows r are the biases' sums, rows r + 8 (the scales') are not used.
+  // With PREC the remainders of the biases' rounding (bias + Z scale needs more than fp16's 11 bits wherever a
+  // group is not nearly symmetric about zero) follow as [granule][group][c][tokens 4c, 4c + 1; 4c + 2, 4c + 3],
+  // times 2^kLogB to keep them above fp16's subnormals, and take the scales' place in rows r + 8.
   // Moves a group's power of two first where one of them does not fit.
   static __device__ __forceinline__ void convert_meta(const unsigned char *sm, unsigned char *buf, State &s) {
     const int lane = threadIdx.x & 31;
@@ -514,10 +524,9 @@ struct Kernel {
                   for (int k = 0; k < 4; k++) s.acc[j * MPB + u2][t][k] *= f;
           if ((lane >> 2) == i)
 #pragma unroll
-            for (int t = 0; t < NT; t++) {
-              s.bacc[t][0] *= f;
-              s.bacc[t][1] *= f;
-            }
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+              for (int k = 0; k < (PREC ? 4 : 2); k++) s.bacc[t][k] *= f;
         }
       }
     }
@@ -528,20 +537,32 @@ struct Kernel {
       const float z = (float)(1 << (BITS - 1)) * s.fb[k];
       const float s0 = bf_lo(su[k]), s1 = bf_hi(su[k]);
       if (kMW % 32 == 0 || i < kMW) {
-        const uint32_t b = pack_h2(fmaf(s0, z, bf_lo(bu[k]) * s.fb[k]), fmaf(s1, z, bf_hi(bu[k]) * s.fb[k]));
+        const float b0 = fmaf(s0, z, bf_lo(bu[k]) * s.fb[k]), b1 = fmaf(s1, z, bf_hi(bu[k]) * s.fb[k]);
+        const uint32_t b = pack_h2(b0, b1);
         *reinterpret_cast<uint2 *>(buf + hg * 64 + pair * 8) = make_uint2(b, pack_h2(s0 * s.fs[k], s1 * s.fs[k]));
+        if constexpr (PREC) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+          *reinterpret_cast<uint32_t *>(buf + 8 * kMW + hg * 32 + pair * 4) =
+              pack_h2((b0 - f.x) * (float)(1 << kLogB), (b1 - f.y) * (float)(1 << kLogB));
+        }
       }
     }
     __syncwarp();
   }
 
   // Values of a granule: sum of P * (bias + Z scale) a group, and P * scale against the codes.
+  // meta, rest: the granule's part of convert_meta's buffer, and of the remainders behind it.
   static __device__ __forceinline__ void values(const unsigned char *sm, const unsigned char *meta,
-                                                const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2], State &s) {
+                                                const unsigned char *rest, const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2], State &s) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     {
       // one MMA: row g of A = group g's (rows of lanes r >= NG repeat them and are not used)
-      const uint4 m = *reinterpret_cast<const uint4 *>(meta + (r % NG) * 64 + c * 16);
+      uint4 m = *reinterpret_cast<const uint4 *>(meta + (r % NG) * 64 + c * 16);
+      if constexpr (PREC) {
+        const uint2 lo = *reinterpret_cast<const uint2 *>(rest + (r % NG) * 32 + c * 8);
+        m.y = lo.x;
+        m.w = lo.y;
+      }
 #pragma unroll
       for (int t = 0; t < NT; t++) {
         mma(s.bacc[t], m.x, m.y, m.z, m.w, ph[t][0], ph[t][1]);
@@ -653,6 +674,7 @@ struct Kernel {
           s.m10[t][e] = m;
           s.l[t][e] *= f;
           s.bacc[t][e] *= f;
+          if constexpr (PREC) s.bacc[t][e + 2] *= f;
 #pragma unroll
           for (int i = 0; i < VB * MPB; i++) {
             s.acc[i][t][e] *= f;
@@ -685,7 +707,8 @@ struct Kernel {
       }
     convert_meta(sm, meta, s);
 #pragma unroll
-    for (int h = 0; h < UG; h++) values(sm + h * GB, meta + h * 64 * NG, ph[h], pl[h], s);
+    for (int h = 0; h < UG; h++)
+      values(sm + h * GB, meta + h * 64 * NG, meta + 8 * kMW + h * 32 * NG, ph[h], pl[h], s);
   }
 
   // Writes this warp's sums (value units, over 2^kLogP) and max / total to the join buffer.
@@ -706,7 +729,9 @@ struct Kernel {
         }
 #pragma unroll
         for (int g = 0; g < NG; g++) {
-          const float bias = __shfl_sync(kFull, s.bacc[t][e], g * 4 + c);
+          float b = s.bacc[t][e];
+          if constexpr (PREC) b = fmaf(s.bacc[t][e + 2], 1.0f / (1 << kLogB), b);
+          const float bias = __shfl_sync(kFull, b, g * 4 + c);
           const float fe = p2(s.E[g]);
 #pragma unroll
           for (int j = g * GS / DB; j < (g + 1) * GS / DB; j++) {
@@ -1179,9 +1204,9 @@ gwb_status run_attn(attn::Args a, int64_t ws_bytes, cudaStream_t st) {
   using K = attn::Kernel<BITS, D, GS, NT, PREC>;
   auto kern = attn::k_attn_decode<BITS, D, GS, NT, PREC>;
   constexpr size_t join = K::kJoin + attn::kWarps * K::kMeta + K::kQ;   // (all multiples of 16)
-  // ring depth: what lets the CTAs that the registers allow share an SM (227 KB less 1 KB a CTA and the
-  // kernel's static part), at least 2 slots, at most 6
-  constexpr size_t slot = (size_t)attn::kWarps * K::kSlot, most = 227 * 1024 / attn::min_ctas(D, NT) - 1536;
+  // ring depth: what lets the CTAs that the registers allow share an SM (228 KB; a CTA takes 1 KB and the
+  // kernel's static part besides), at least 2 slots, at most 6
+  constexpr size_t slot = (size_t)attn::kWarps * K::kSlot, most = 228 * 1024 / attn::min_ctas(D, NT) - 1536;
   int depth = join < most ? (int)((most - join) / slot) : 0;
   depth = depth < 2 ? 2 : (depth > 6 ? 6 : depth);
   const size_t smem = join + depth * slot;

@@ -166,7 +166,24 @@ def read_rows(cache, slots, what, bits, D, gs, page):
 
 
 # ------------------------------------------------------------------ attention
-def attn_decode(q, cache, table, lens, bits, gs, page, scale, f16):
+def exact_score_rows(rng, T, H, D, gs, values):
+    """(k, v) [T, H, D] as bf16 values for attention whose scores leave no room for an error of their own: column 0
+    of every key is n / 64, n whole, in a group that holds 0 and 255 / 64 (an 8-bit scale of 2^-6 and a bias of 0),
+    so a query of 2^j in column 0 and zeros elsewhere meets one exact product a token.  `values`: how v is drawn."""
+    k = bf16(np.abs(rng.standard_normal((T, H, D)))).clip(0, 3.5)
+    k[..., ::gs], k[..., 1::gs], k[..., 2::gs] = 0.0, 255 / 64, 0.0
+    k[..., 0] = rng.integers(0, 256, (T, H)) / 64
+    v = rng.standard_normal((T, H, D))
+    if values != "symmetric":
+        v = np.abs(v)                                # the group's minimum is small beside its range
+    if values == "outliers":
+        v[..., ::40] *= 30
+    if values == "shifted":
+        v += 33.0                                    # the range is small beside the mean
+    return k, bf16(v)
+
+
+def attn_decode(q, cache, table, lens, bits, gs, page, scale, f16, exact_scores=False):
     """(out, lse, bound, lse_bound): out [B, HQ, D] and lse [B, HQ] in fp64; bound [B, HQ, D]: how far an
     implementation may be off that forms the scores in fp32 and rounds the softmax weights, their product
     with a value scale and the centred bias to fp16 (pairs of fp16 if f16), and its result to the output type.
@@ -178,6 +195,9 @@ def attn_decode(q, cache, table, lens, bits, gs, page, scale, f16):
       range    weights below 2^-24 of the largest lose bits: N * 2^-29 of the largest value
       sums     fp32, truncated, over at most N / 16 MMAs and 64 joins: 2 u (N / 16 + 64) of the magnitudes
       output   half a step: 2^-8 (bf16), 2^-11 (fp16), of the result
+    exact_scores: q and k are such that the sums are exact (exact_score_rows, or a zero query), which leaves the
+    roundings of x = scale q . k and of its distance from the maximum (up to 16 in log2 units):
+    e_t = 4 u (|x_t| + 16) + 2^-21.
     lse_bound [B, HQ]: log-sum-exp moves by no more than the largest score error (it is 1-Lipschitz in the
     maximum norm), plus its total's fp32 sum, 2 u (N / 32 + 64) relative, and its own roundings, 4 u (|lse| + 16).
     """
@@ -209,7 +229,7 @@ def attn_decode(q, cache, table, lens, bits, gs, page, scale, f16):
             w = p / p.sum()
             out[b, h], lse[b, h] = w @ v, m + np.log(p.sum())
             T = abs(scale) * ((kc[:, kv] * np.abs(rep(ks[:, kv])) + np.abs(rep(kb[:, kv]))) @ np.abs(q[b, h]))
-            e = 2 * u * (D + 16) * T + 2.0 ** -21
+            e = (4 * u * (np.abs(x) + 16) if exact_scores else 2 * u * (D + 16) * T) + 2.0 ** -21
             lse_bound[b, h] = e.max() + 2 * u * (len(t) / 32 + 64) + 4 * u * (abs(lse[b, h]) + 16)
             a = np.abs(vc[:, kv] - Z) * rep(np.abs(vs[:, kv])) + np.abs(rep(vb[:, kv] + Z * vs[:, kv]))
             mag = np.abs(v) + a

@@ -779,3 +779,45 @@ def test_a_decode_step_through_the_layer():
     assert (np.abs(_np(a) - ref) <= bound).all()
     q_o, s_o, h_o = S.rmsnorm_quant_i8(_np(o), _np(h), w2, 1e-5, False)
     assert np.array_equal(q2.cpu().numpy(), q_o) and np.array_equal(s2.cpu().numpy(), s_o) and np.array_equal(_np(h2), h_o)
+
+
+# ------------------------------------------------------------------ what fp16 outputs promise
+@pytest.mark.parametrize("values", ["symmetric", "small minimum", "outliers", "shifted"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("bits,D,gs,G", [(8, 64, 32, 4), (8, 128, 64, 3), (8, 128, 128, 12), (8, 256, 64, 8)])
+def test_attention_weights_and_values_where_scores_are_exact(bits, D, gs, G, dt, values):
+    """Scores without an error of their own, few tokens: what is left is how weights, their products with the value
+    scales and the centred biases are rounded (oracle.serving.attn_decode, exact_scores)."""
+    _exact_scores([1, 2, 3, 5, 2, 3], 2, G, D, bits, gs, dt, values, 1.0)
+
+
+@pytest.mark.parametrize("values", ["symmetric", "small minimum", "outliers", "shifted"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("bits,D,gs,G", [(4, 64, 64, 4), (4, 128, 32, 9), (4, 256, 128, 2), (8, 128, 32, 8), (8, 64, 64, 16)])
+def test_attention_values_under_a_zero_query(bits, D, gs, G, dt, values):
+    """Equal weights: the mean of the rows, exact but for the biases, the products with the scales and the output."""
+    _exact_scores([1, 500, 2, 17, 700], 2, G, D, bits, gs, dt, values, 0.0)
+
+
+def _exact_scores(lens, H, G, D, bits, gs, dt, values, q0):
+    rng = np.random.default_rng(1000 * bits + D + gs + G)
+    page = 32
+    need = [-(-n // page) for n in lens]
+    table = np.zeros((len(lens), max(need)), dtype=np.int32)
+    order, at, slots = rng.permutation(sum(need)), 0, []
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+        t = np.arange(lens[b])
+        slots.append(table[b][t // page].astype(np.int64) * page + t % page)
+    slots = np.concatenate(slots)
+    k, v = S.exact_score_rows(rng, len(slots), H, D, gs, values)
+    q = np.zeros((len(lens), H * G, D))
+    q[..., 0] = q0 * 2.0 ** -rng.integers(0, 2, q.shape[:2])
+    cache = gwb.kv_cache(sum(need), H, D, page, bits, gs)
+    gwb.kv_write(cache, torch.tensor(slots).to(DEV), _t(k, "bf16"), _t(v, "bf16"), bits, gs)
+    args = (_t(q, dt), cache, torch.tensor(table).to(DEV), torch.tensor(np.array(lens, dtype=np.int32)).to(DEV), bits, gs)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = gwb.attn_decode(*args, scale=1.0, lse=lse)
+    ref = S.attn_decode(q, cache.cpu().numpy(), table, lens, bits, gs, page, 1.0, dt == "fp16", exact_scores=True)
+    _compare(_np(out), _np(lse), *ref)

@@ -251,3 +251,51 @@ def test_attention_pins():
     assert (out[2] == 0).all() and np.isneginf(lse[2]).all() and (bound[2] == 0).all() and (lse_bound[:2] > 0).all()
     # half a step of a range of up to 8, and the bf16 roundings of scale and bias (2^-9 of range and minimum)
     assert np.abs(kd - k[at]).max() < 8 / 255 / 2 + 8 * 2.0 ** -9 + 4 * 2.0 ** -9 and (bound[:2] > 0).all()
+
+
+# ------------------------------------------------------------------ what the attention's bound tells apart
+def _one_row(values, seed):
+    """Largest error over bound of fp16 attention restated in numpy (8 bits, D 128, groups of 64, 3 tokens, one
+    head): with the remainders of the weights' and of the biases' fp16 rounding taken along, without the weights',
+    without the biases'."""
+    rng = np.random.default_rng(seed)
+    bits, D, gs, page = 8, 128, 64, 16
+    k, v = S.exact_score_rows(rng, 3, 1, D, gs, values)
+    cache = np.zeros((1, 1, S.Layout(bits, D, gs).bytes), dtype=np.uint8)
+    S.write_rows(cache, np.arange(3), k, "k", bits, gs, page)
+    S.write_rows(cache, np.arange(3), v, "v", bits, gs, page)
+    q = np.zeros((1, 1, D))
+    q[..., 0] = 1.0
+    ref, _, bound, _ = S.attn_decode(q, cache, np.zeros((1, 1), dtype=np.int32), [3], bits, gs, page, 1.0, True,
+                                     exact_scores=True)
+    h = lambda x: np.asarray(x, dtype=np.float16).astype(np.float64)  # noqa: E731
+    code, s, b = (x[:, 0] for x in S.parts_of(cache, np.arange(3), "v", bits, D, gs, page))
+    x = S.read_rows(cache, np.arange(3), "k", bits, D, gs, page)[:, 0, 0]
+    assert np.array_equal(x, k[:, 0, 0])             # the keys' column is exact
+    p = 2.0 ** 10 * np.exp(x - x.max())
+    # scales and biases over the power of two that holds both
+    e = 2.0 ** np.ceil(np.log2(np.maximum(s * 2 ** bits, np.abs(b)).max(0)) + 1)
+    sc, bi = s / e * 2 ** bits, (b + 128 * s) / e
+    worst = []
+    for weights, biases in ((1, 1), (0, 1), (1, 0)):
+        hi = h(p)
+        lo = weights * h(p - hi)
+        ps = h(hi[:, None] * sc)
+        pl = weights * h(lo[:, None] * sc + h(hi[:, None] * sc - ps))
+        bh = h(bi)
+        bl = biases * h((bi - bh) * 2 ** 11) / 2 ** 11
+        o = ((np.repeat(ps + pl, gs, 1) * (code - 128)).sum(0) / 2 ** bits
+             + np.repeat(((hi + lo)[:, None] * (bh + bl)).sum(0), gs)) * np.repeat(e, gs) / p.sum()
+        worst.append((np.abs(h(o) - ref[0, 0]) / bound[0, 0]).max())
+    return worst
+
+
+@pytest.mark.parametrize("values", ["symmetric", "small minimum", "outliers", "shifted"])
+def test_attention_bound_sees_a_lost_remainder(values):
+    """fp16 outputs keep within the bound of exact scores with every remainder, and leave it without the weights'
+    or (where a bias does not fit fp16) the biases'."""
+    both, no_weights, no_biases = np.max([_one_row(values, seed) for seed in range(6)], axis=0)
+    assert both <= 1.0
+    assert no_weights > 1.05
+    if values != "symmetric":
+        assert no_biases > 1.05
