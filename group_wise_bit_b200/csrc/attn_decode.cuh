@@ -775,7 +775,7 @@ __device__ __forceinline__ float lse_of(float m10, float l) {
 template <int BITS, int D, int GS, int NT, bool PREC>
 __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const Args a) {
   using K = Kernel<BITS, D, GS, NT, PREC>;
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ uint64_t bars[kWarps * 8];
   __shared__ Start start;
   __shared__ long long scan[kWarps];

@@ -1,6 +1,9 @@
 """CPU checks of the norm, the quantized paged cache and the decode attention: what their entry points
 refuse on the host, and pins of the oracle the GPU tests compare with."""
 import ctypes
+import glob
+import os
+import re
 
 import numpy as np
 import pytest
@@ -299,3 +302,17 @@ def test_attention_bound_sees_a_lost_remainder(values):
     assert no_weights > 1.05
     if values != "symmetric":
         assert no_biases > 1.05
+
+
+# ------------------------------------------------------------------ shared memory
+def test_dynamic_shared_memory_states_its_alignment():
+    """Vector accesses, cp.async and bulk copies need 16 bytes: each kernel's dynamic buffer says so, whatever the
+    size of the static variables in front of it."""
+    found = 0
+    for src in sorted(glob.glob(os.path.join(gbuild.CSRC, "*.cu*"))):
+        for line in open(src):
+            if "extern __shared__" in line:
+                m = re.search(r"__align__\((\d+)\)", line)
+                assert m and int(m.group(1)) % 16 == 0, f"{os.path.basename(src)}: {line.strip()}"
+                found += 1
+    assert found >= 8
