@@ -964,7 +964,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
         }
       }
       // per-head constants for the score fragment's columns 2c, 2c + 1
-      const float back = a.scale_log2 * pow2f(24 - up < -126 ? -126 : (24 - up > 127 ? 127 : 24 - up));
+      // (two factors: 24 - up passes 127 for a query beyond 2^115, and only the product may overflow)
+      const float back = a.scale_log2 * pow2f(12) * pow2f(12 - up);
 #pragma unroll
       for (int g = 0; g < K::NG; g++) {
         part[g] += __shfl_xor_sync(kFull, part[g], 1);

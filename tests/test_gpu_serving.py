@@ -821,3 +821,35 @@ def _exact_scores(lens, H, G, D, bits, gs, dt, values, q0):
     out = gwb.attn_decode(*args, scale=1.0, lse=lse)
     ref = S.attn_decode(q, cache.cpu().numpy(), table, lens, bits, gs, page, 1.0, dt == "fp16", exact_scores=True)
     _compare(_np(out), _np(lse), *ref)
+
+
+# ------------------------------------------------------------------ queries and scores at the end of fp32's range
+@pytest.mark.parametrize("D,bits,G", [(64, 8, 4), (128, 8, 9), (256, 8, 2)])
+@pytest.mark.parametrize("lens", [[3, 40, 300], [700, 1, 0, 90]])
+def test_attention_of_very_large_queries(lens, D, bits, G):
+    """Queries times 2^117 over keys over 2^117 are the same scores, bit for bit."""
+    rng = np.random.default_rng(D)
+    k, v = S.exact_score_rows(rng, sum(lens), 1, D, 64, "symmetric")
+    q = np.zeros((len(lens), G, D))
+    q[..., 0] = 2.0 ** -rng.integers(0, 3, q.shape[:2])
+    got = []
+    for up in (0, 117):
+        args = _one_head_batch(k * 2.0 ** -up, v, q * 2.0 ** up, lens, bits, 64)
+        lse = torch.empty(q.shape[:2], device=DEV)
+        got.append((gwb.attn_decode(*args, lse=lse), lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.isfinite(got[0][0]).all()
+
+
+def _one_head_batch(k, v, q, lens, bits, gs, page=32):
+    """Arguments of attn_decode for rows k, v [sum(lens), 1, D] in consecutive pages, bf16."""
+    need = [-(-n // page) for n in lens]
+    table = np.zeros((len(lens), max(need)), dtype=np.int32)
+    at, slots = 0, []
+    for b, n in enumerate(need):
+        table[b, :n] = np.arange(at, at + n)
+        slots.append(at * page + np.arange(lens[b]))
+        at += n
+    cache = gwb.kv_cache(sum(need), 1, q.shape[2], page, bits, gs)
+    gwb.kv_write(cache, torch.tensor(np.concatenate(slots)).to(DEV), _t(k, "bf16"), _t(v, "bf16"), bits, gs)
+    return (_t(q, "bf16"), cache, torch.tensor(table).to(DEV), torch.tensor(np.array(lens, dtype=np.int32)).to(DEV), bits, gs)
