@@ -723,6 +723,7 @@ struct Kernel {
         l += __shfl_xor_sync(kFull, l, 8);
         l += __shfl_xor_sync(kFull, l, 16);
         const int h = 8 * t + 2 * c + e;
+        if (s.m10[t][e] == INFINITY) l = NAN;       // a score beyond fp32: every p is 0 beside it
         if (r == 0) {
           row_ml[2 * h] = s.m10[t][e];
           row_ml[2 * h + 1] = l;

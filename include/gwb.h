@@ -436,6 +436,8 @@ gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t 
  * A key that is not finite makes the rows of its sequence and kv head NaN, a
  * value its group of their columns; what lies behind a sequence's end or on
  * pages that it does not name is never read into a sum.
+ * A query that is not finite, or a score (times log2 e) above fp32's largest
+ * number, makes its row NaN; so may scores below its lowest.
  * Range: |scale * q| below 2^115; values below 2^114 over the number of tokens
  * (else infinities or NaN).  A value's rounding is relative down to 2^-14 of the
  * largest that its group's column holds in the sequence, whatever that one's

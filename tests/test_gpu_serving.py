@@ -841,6 +841,37 @@ def test_attention_of_very_large_queries(lens, D, bits, G):
     assert torch.isfinite(got[0][0]).all()
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("lens", [[3, 40, 300], [700, 1, 0, 90]])
+def test_attention_scores_beyond_fp32_are_not_silently_zeros(lens, sign):
+    """Every score overflows: NaN rows and log-sum-exps, not the zeros of an empty row."""
+    rng = np.random.default_rng(3)
+    k, v = S.exact_score_rows(rng, sum(lens), 1, 128, 64, "symmetric")
+    k[..., 0] = np.maximum(k[..., 0], 1 / 64)
+    q = np.zeros((len(lens), 4, 128))
+    q[..., 0] = sign * 2.0 ** 100
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = gwb.attn_decode(*_one_head_batch(k * 2.0 ** 40, v, q, lens, 8, 64), lse=lse)
+    full = torch.tensor([n > 0 for n in lens], device=DEV)
+    assert torch.isnan(out[full]).all() and torch.isnan(lse[full]).all()
+    assert not out[~full].any() and torch.isneginf(lse[~full]).all()
+
+
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("lens,dt,bits,G", [([40, 700, 3], "bf16", 4, 4), ([40, 300, 3], "fp16", 8, 4),
+                                            ([40, 700, 3], "fp16", 4, 12), ([40, 300, 3], "bf16", 8, 2)])
+def test_attention_queries_that_are_not_finite_make_their_rows_nan(lens, dt, bits, G, value):
+    b = Batch(lens, 2, G, 128, bits, 64, 64, dt, seed=22)
+    good, good_lse = b.run()
+    for i, h in ((1, 0), (0, G), (2, 2 * G - 1)):
+        b.args[0][i, h, 37] = float(value)
+    out, lse = b.run()
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[1, 0] = hit[0, G] = hit[2, 2 * G - 1] = True
+    assert torch.equal(torch.isnan(lse), hit) and torch.equal(torch.isnan(out), hit[..., None].expand_as(out))
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], good_lse[~hit])
+
+
 def _one_head_batch(k, v, q, lens, bits, gs, page=32):
     """Arguments of attn_decode for rows k, v [sum(lens), 1, D] in consecutive pages, bf16."""
     need = [-(-n // page) for n in lens]
