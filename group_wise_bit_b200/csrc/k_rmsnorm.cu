@@ -2,7 +2,7 @@
 // one scale a token, in one pass over the activations:
 //
 //   h = x + residual, rounded once to the activations' type (and stored)
-//   r = 1 / sqrt(mean(h^2) + eps)            sum and root in fp64, rounded once to fp32
+//   r = 1 / sqrt(mean(h^2) + eps)            sum and root in fp64, rounded once to fp32; 0 for a row of zeros
 //   y = (h * r) * weight                     fp32, one rounding a product
 //   sx = max|y| / 127;  qx = clip(rint(y / sx), -127, 127)
 //
@@ -89,7 +89,7 @@ __device__ __forceinline__ float block_rstd(double sum, double *red, float *out,
   __syncthreads();
   if (warp == 0) {
     const double t = warp_sum(lane < nw ? red[lane] : 0.0);
-    if (lane == 0) *out = (float)(1.0 / sqrt(t / (double)K + eps));
+    if (lane == 0) *out = t == 0.0 ? 0.0f : (float)(1.0 / sqrt(t / (double)K + eps));   // (0 * inf is no norm)
   }
   __syncthreads();
   return *out;

@@ -347,7 +347,7 @@ gwb_status gwb_gemm_i8i8(const int8_t *qx, const float *sx, int64_t M, const int
  * the dynamic per-token int8 activations of gwb_gemm_i8i8 / gwb_gemm_i8i4 as its
  * output:
  *   h  = residual ? round(x + residual) : x        (rounded once to `dtype`; stored)
- *   r  = fp32(1 / sqrt(mean_k h[m,k]^2 + eps))     (sum and root in fp64)
+ *   r  = fp32(1 / sqrt(mean_k h[m,k]^2 + eps))     (sum and root in fp64; 0 for a row of zeros, with eps = 0 too)
  *   y  = (h * r) * weight                          (fp32, one rounding a product; not stored)
  *   sx[m] = max_k |y| / 127;  qx[m,k] = clip(round_half_even(y / sx[m]), -127, 127)
  * (0 when the row of y is zero).  The quantizer is gwb_quant_per_token_i8's, on

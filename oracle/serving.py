@@ -41,7 +41,8 @@ def rmsnorm_quant_i8(x, residual, weight, eps, f16):
     """(qx int8, sx fp32, h): every step of the definition, fp32 where it says fp32."""
     x = np.asarray(x, dtype=np.float64)
     h = x if residual is None else rnd((x + residual).astype(np.float32), f16)
-    r = np.array([1.0 / np.sqrt(np.sum(np.square(row)) / row.size + eps) for row in h], dtype=np.float32)
+    r = np.array([1.0 / np.sqrt(np.sum(np.square(row)) / row.size + eps) if row.any() else 0.0 for row in h],
+                 dtype=np.float32)
     f32 = np.float32
     with np.errstate(all="ignore"):
         y = (h.astype(f32) * r[:, None]).astype(f32) * np.asarray(weight).astype(f32)

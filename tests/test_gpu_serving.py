@@ -884,3 +884,22 @@ def _one_head_batch(k, v, q, lens, bits, gs, page=32):
     cache = gwb.kv_cache(sum(need), 1, q.shape[2], page, bits, gs)
     gwb.kv_write(cache, torch.tensor(np.concatenate(slots)).to(DEV), _t(k, "bf16"), _t(v, "bf16"), bits, gs)
     return (_t(q, "bf16"), cache, torch.tensor(table).to(DEV), torch.tensor(np.array(lens, dtype=np.int32)).to(DEV), bits, gs)
+
+
+# ------------------------------------------------------------------ rows of zeros without eps
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K", [(4, 1), (4, 77), (5, 4096), (700, 520), (3, 40000)])
+def test_norm_of_a_zero_row_with_eps_zero(M, K, dt):
+    """Scale 0 and codes 0, as with any other eps; the rows beside it keep their results."""
+    rng = np.random.default_rng(K)
+    x, w = _rand(rng, (M, K), dt), S.rnd(1 + 0.1 * rng.standard_normal(K), dt == "fp16")
+    x[0], x[2] = 0.0, -0.0
+    r = _rand(rng, (M, K), dt)
+    r[0], r[2] = 0.0, 0.0
+    r[1] = -x[1]                                      # a sum of zeros
+    for res in (None, r):
+        q, s, h = gwb.rmsnorm_quant_i8(_t(x, dt), _t(w, dt), 0.0, residual=None if res is None else _t(res, dt))
+        zero = [0, 2] if res is None else [0, 1, 2]
+        assert not s[zero].any() and not q[zero].any()
+    _check_norm(x, None, w, dt, eps=0.0)
+    _check_norm(x, r, w, dt, eps=0.0)

@@ -316,3 +316,9 @@ def test_dynamic_shared_memory_states_its_alignment():
                 assert m and int(m.group(1)) % 16 == 0, f"{os.path.basename(src)}: {line.strip()}"
                 found += 1
     assert found >= 8
+
+
+def test_norm_of_zeros_without_eps_is_zero():
+    q, s, _ = S.rmsnorm_quant_i8(np.array([[0.0, -0.0], [3.0, -4.0]]), None, np.ones(2), 0.0, False)
+    r = np.float32(1 / np.sqrt(12.5))
+    assert s[0] == 0 and not q[0].any() and q[1].tolist() == [95, -127] and s[1] == np.float32(4) * r / np.float32(127)
