@@ -556,9 +556,10 @@ def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, ou
     out = _out_of(out, "out", q, (B, HQ, D), q.dtype)
     if lse is not None:
         _dev(lse, "lse", (torch.float32,), (B, HQ))
-    stream = _stream_of(q, cache, page_table, seq_lens, out, lse, workspace)
     if workspace is not None:
         _dev(workspace, "workspace", (torch.uint8,))
+    stream = _stream_of(q, cache, page_table, seq_lens, out, lse, workspace)
+    if workspace is not None:
         ws = workspace.numel()
     else:
         ws = attn_decode_workspace(HQ, heads, D, B, max_pages * page_size)

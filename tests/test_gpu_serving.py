@@ -903,3 +903,11 @@ def test_norm_of_a_zero_row_with_eps_zero(M, K, dt):
         assert not s[zero].any() and not q[zero].any()
     _check_norm(x, None, w, dt, eps=0.0)
     _check_norm(x, r, w, dt, eps=0.0)
+
+
+def test_attention_refuses_a_workspace_that_is_no_tensor():
+    b = Batch([3], 1, 1, 64, 4, 32, 16, "bf16")
+    for bad, error in ((1 << 20, TypeError), (torch.empty(1 << 20, device=DEV), TypeError),
+                       (torch.empty(1 << 20, dtype=torch.uint8), ValueError)):
+        with pytest.raises(error, match="workspace"):
+            gwb.attn_decode(*b.args, workspace=bad)
