@@ -911,3 +911,25 @@ def test_attention_refuses_a_workspace_that_is_no_tensor():
                        (torch.empty(1 << 20, dtype=torch.uint8), ValueError)):
         with pytest.raises(error, match="workspace"):
             gwb.attn_decode(*b.args, workspace=bad)
+
+
+# ------------------------------------------------------------------ every instance with 16-head tiles
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("bits,D,gs", [x for x in LAYOUTS if x[1] <= 128])
+def test_attention_layouts_with_more_than_eight_heads(bits, D, gs, dt):
+    """Groups of 9 to 16 query heads a kv head share a tile of 16; 12 and 20 leave rows of it empty or take two."""
+    seed = bits + D + gs
+    Batch([700, 1, 0, 33, 16], 2, 12, D, bits, gs, 16, dt, seed=seed).check()          # cut
+    Batch([0, 1, 31, 300], 1, 16, D, bits, gs, 64, dt, seed=seed).check()              # a CTA a pair
+    lens = np.random.default_rng(seed).integers(0, 40, 260)
+    b = Batch(lens, 1, 20, D, bits, gs, 32, dt, seed=seed)                             # a warp a pair
+    b.check()
+    gwb.check_device_error()
+
+
+@pytest.mark.parametrize("bits,D,gs", [x for x in LAYOUTS if x[1] <= 128])
+def test_sixteen_head_tiles_round_as_eight_head_ones(bits, D, gs):
+    """fp16, exact scores: the bound of the roundings alone (see above) on every 16-head instance."""
+    for q0 in ((1.0, 0.0) if bits == 8 else (0.0,)):
+        _exact_scores([1, 2, 3, 5], 1, 16, D, bits, gs, "fp16", "outliers", q0)
+        _exact_scores([600, 3], 1, 9, D, bits, gs, "fp16", "small minimum", q0)
