@@ -91,7 +91,7 @@ struct Args {
   int min_per;                  // least places of a share
   int f16;
   int mode;                     // AttnMode
-  float scale_log2;             // softmax scale * log2 e
+  float scale_log2;             // softmax scale * log2 e * 2^12
 };
 
 // One record a CTA, for the join: the pair that the boundary in front of its share cuts, where no
@@ -965,8 +965,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas(D, NT)) k_attn_decode(const
         }
       }
       // per-head constants for the score fragment's columns 2c, 2c + 1
-      // (two factors: 24 - up passes 127 for a query beyond 2^115, and only the product may overflow)
-      const float back = a.scale_log2 * pow2f(12) * pow2f(12 - up);
+      // (2^(24 - up), of which 2^12 came with the scale: 24 - up passes 127 for a query beyond 2^115, and only
+      // the product may overflow)
+      const float back = a.scale_log2 * pow2f(12 - up);
 #pragma unroll
       for (int g = 0; g < K::NG; g++) {
         part[g] += __shfl_xor_sync(kFull, part[g], 1);
@@ -1196,7 +1197,7 @@ attn::Args attn_args(const AttnCall &c) {
   a.cap = (int)(cap < 0x7fffff00 ? cap : 0x7fffff00);          // (a whole number of units)
   a.min_per = attn::kWarps;
   a.f16 = c.f16;
-  a.scale_log2 = c.scale * 1.4426950408889634f;
+  a.scale_log2 = c.scale * 1.4426950408889634f * 4096.0f;
   return a;
 }
 
