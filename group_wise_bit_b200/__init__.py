@@ -533,8 +533,8 @@ def attn_decode_workspace(q_heads, heads, head_dim, batch=0, max_tokens=0):
 def attn_decode(q, cache, page_table, seq_lens, bits, group_size, scale=None, out=None, lse=None, workspace=None):
     """Attention of one new token a sequence over the quantized cache: [B, q_heads, head_dim] of q's dtype.
 
-    q [B, q_heads, head_dim] (bf16 or fp16, any sequence stride), page_table int32 [B, max_pages] (any row
-    stride), seq_lens int32 [B] (0: an empty row, zeros).  scale defaults to 1 / sqrt(head_dim).  lse, if
+    q [B, q_heads, head_dim] (bf16 or fp16, any sequence stride), page_table int32 [B, max_pages] (rows may lie
+    apart, not overlap), seq_lens int32 [B] (0: an empty row, zeros).  scale defaults to 1 / sqrt(head_dim).  lse, if
     given, is an fp32 [B, q_heads] output.  workspace: a uint8 tensor of attn_decode_workspace() bytes that
     no overlapping call uses; without one the call takes it from torch's allocator."""
     qs = _token_rows(q, "q", None, _HALVES)

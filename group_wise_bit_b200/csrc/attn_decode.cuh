@@ -32,10 +32,12 @@
 //
 // What bounds it.  8-bit caches: memory (64 sequences of up to 8192 tokens, 8 kv
 // heads x 128, 64 query heads: 132 us = 6.1 TB/s, 0.93 of a plain copy).  4-bit
-// caches: the SM's work a token (the same at 4 bits: 101 us = 4.2 TB/s): about 285
-// issue slots a granule, 80 of them masks and shifts of codes, 25 MMAs; the copies
-// alone would take 80 us of 104 at 8 sequences of 65536 tokens.  Short calls: the
-// chain lengths, page ids, codes, queries, join (1 sequence of 128 tokens: 5 us).
+// caches: the latency of dependent instructions in 12 warps an SM (the same at 4
+// bits: 102 us = 4.2 TB/s).  A granule takes 286 issue slots, 80 of them masks and
+// shifts of codes, 25 MMAs, where memory's time would leave room for 383; slots are
+// 52 % busy, the tensor pipe 34 %, and the first stall is the fixed latency (31 %).
+// fp16 outputs (PREC) add MMAs: 126 us at 4 bits, 146 at 8.  Short calls: the chain
+// lengths, page ids, codes, queries, join (1 sequence of 128 tokens: 5 us).
 // Slower, and left out: e4m3 MMAs for the keys (a nibble is an e4m3 number; 131
 // against 112 us, with more instructions and fp16 MMAs counted, not fewer), a
 // granule's values beside the next one's scores (117), four CTAs an SM (115), the
@@ -302,8 +304,10 @@ __device__ __forceinline__ void cursor_settle(const Args &a, Cursor &c, int firs
 // products; one where two rings of two would leave an SM with one CTA (8 bits, head_dim 256).
 constexpr int unit_granules(int granule) { return granule > 8192 ? 1 : 2; }
 
-// Resident CTAs an SM that the registers are held to: 16 warps where 128
-// registers a thread hold the state, 8 where it takes more.
+// Resident CTAs an SM that the registers are held to: 12 warps where 168
+// registers a thread hold the state, 8 (255 registers) where it takes more.  Shared
+// memory may allow fewer: 8 bits at head_dim 128 has ring slots of 35 KB for its
+// four warps, and two CTAs fit.
 constexpr int min_ctas(int D, int NT) { return D * NT <= 128 ? 3 : 2; }
 
 template <int BITS, int D, int GS, int NT, bool PREC>

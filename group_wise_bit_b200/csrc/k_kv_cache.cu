@@ -11,9 +11,16 @@
 // Where a block's 16 slots are one granule, as in a prompt, its codes and metadata
 // go through shared memory in the cache's order and move in 16-byte pieces; else
 // every thread moves its own 2- and 4-byte units.  8192 tokens of 8 heads x 128 at
-// 8 bits: write 13.2 us, read 13.7 us, against 8 us each for their 51 MB; the issue
-// slots bound both (the write's min, max, quotient and rounding are 23 operations
-// an element; it took 34 us with 8 elements a thread and 2-byte stores).
+// 8 bits, every buffer out of L2: write 13.2 us (13.7 from slices of a fused
+// projection), read 13.8, against 7.9 each for their 51 MB; at 4 bits 12.5 and 12.9
+// against 6.6; 32768 tokens at 8 bits 44 and 46 against 31.5.  A last tile that is
+// no whole granule costs the write 4 us more (8155 tokens: 17.6), its block's small
+// units head after head; tiles of padding cost nothing.  The write spends 18 issue
+// slots an element, about 8 of them the quantizer's (unpacking, min, max, quotient,
+// rounding, packing), the rest addresses, 2-byte staging of the values and barriers,
+// and has 69 % of its active cycles' slots busy; the read spends 12 and has 57 %,
+// with loads and barriers in front of the rest.  (34 us with 8 elements a thread and
+// 2-byte stores.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
