@@ -44,7 +44,7 @@
 // shifts as multiplications (121), shares half or a third as long (118, 124).
 //
 // Precision.  q is scaled by a power of two per head into fp16 (exact for bf16
-// and fp16 but for elements 2^-27 below the largest).  Scores, maxima, totals
+// and fp16 but for elements 2^-22 below the largest).  Scores, maxima, totals
 // and outputs are fp32; a score's MMA truncates at 2^-14 of a code step of its
 // largest |q|, well below what fp16 does to p.  p is rounded to fp16 (2^-11) before it meets the codes,
 // p * sv again, and the centred bias bv + Z sv too: 2^-11 of each, against the

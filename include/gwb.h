@@ -429,10 +429,13 @@ gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t 
  * length beyond max_pages * page_size is cut to it, and the 16 tokens of a
  * granule whose page id is outside the cache are left out; both are reported
  * by gwb_check_device_error.  Scores, sums and the softmax are fp32, and codes,
- * key scales, key biases and q enter exactly.  Three things are rounded: the
- * softmax weights, their products with a value scale, and a value group's centre
- * (bias + scale * 2^(bits-1)), each once to fp16 with bf16 outputs (2^-11 of it,
- * against the output's 2^-8) and to fp16 pairs with fp16 outputs (2^-21).
+ * key scales, key biases and q (but for elements 2^-22 below a head's largest)
+ * enter exactly; the tensor core cuts a product of a key code and a query element
+ * at 2^-14 of a code step times the largest |q| of the 16 elements it adds at
+ * once.  Three things are rounded: the softmax weights, their products with a
+ * value scale, and a value group's centre (bias + scale * 2^(bits-1)), each once
+ * to fp16 with bf16 outputs (2^-11 of it, against the output's 2^-8) and to fp16
+ * pairs with fp16 outputs (2^-21).
  * A key that is not finite makes the rows of its sequence and kv head NaN, a
  * value its group of their columns; what lies behind a sequence's end or on
  * pages that it does not name is never read into a sum.
@@ -441,7 +444,7 @@ gwb_status gwb_kv_read(const void *cache, int64_t pages, int64_t heads, int64_t 
  * Range: |scale * q| below 2^115; values below 2^114 over the number of tokens
  * (else infinities or NaN).  A value's rounding is relative down to 2^-14 of the
  * largest that its group's column holds in the sequence, whatever that one's
- * weight, and below that up to 2^-23 of the largest.
+ * weight (and to 2^-114), and below that up to 2^-23 of the largest.
  * Deterministic for given lengths and device. */
 /* Bytes of the workspace on the current device for at most B sequences (0: any number) whose page
  * tables name max_tokens tokens (max_pages * page_size; 0: any): none where such calls cut no sequence,

@@ -192,6 +192,8 @@ def attn_decode(q, cache, table, lens, bits, gs, page, scale, f16, exact_scores=
     With u = 2^-24, weights w_t, value parts a_t = s |code - Z| and b'_t = |bias + Z s| (Z the middle code):
       score    the sum's D + 2 D / gs fp32 steps, truncated by the MMA, each off by at most 2 u of the sum of
                magnitudes T_t = |scale| (sum_d |q_d| (code s + |bias|));  e_t = 2 u (D + 16) T_t + 2^-21
+               (no allowance for products that the MMA cuts at 2^-14 of a code step of the largest |q| beside
+               them, which T_t outweighs unless one |q| passes the others by far and meets small codes)
       weight   e_t twice (numerator and total), and fp16: 2^-11 (pairs: 2^-21) once for w, once for w * s or b'
       range    weights below 2^-24 of the largest lose bits: N * 2^-29 of the largest value
       sums     fp32, truncated, over at most N / 16 MMAs and 64 joins: 2 u (N / 16 + 64) of the magnitudes
